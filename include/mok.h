@@ -150,6 +150,78 @@ mok_status mok_route_topk_gemm(const void* x, const void* w_router, int32_t T, i
                                int32_t E, int32_t k, void* ws, size_t ws_bytes,
                                int32_t* topk_idx, float* topk_gate, hipStream_t stream);
 
+/* Element types of the calls below that take more than one. */
+typedef enum { MOK_TYPE_F32 = 0, MOK_TYPE_BF16 = 1 } mok_type;
+
+/* Scored route: scores of every expert, a bias for balance, groups of experts,
+ * and weights from the scores without the bias. */
+typedef enum { MOK_SCORE_SOFTMAX = 0, MOK_SCORE_SIGMOID = 1 } mok_score;
+typedef enum {
+    MOK_GROUP_MAX = 0,   /* a group counts as its largest choice value           */
+    MOK_GROUP_TOP2 = 1   /* ... as the sum of its two largest (of its only one)  */
+} mok_group_rule;
+
+typedef struct {
+    int32_t n_experts;   /* E, 1..4096                                           */
+    int32_t top_k;       /* k, 1..32, at most top_groups * (E / n_groups)        */
+    int32_t score;       /* mok_score                                            */
+    int32_t n_groups;    /* G equal runs of consecutive experts, 1..64; G | E    */
+    int32_t top_groups;  /* groups a token may pick from, 1..G                   */
+    int32_t group_rule;  /* mok_group_rule (G > 1)                               */
+    int32_t renorm;      /* 1: the picks' scores are divided by their sum        */
+    float scale;         /* factor of every gate, finite                         */
+} mok_router_desc;
+
+/* Scored route.  For each token t with logits l (row t of `logits`, E values
+ * of logits_type, rows ld elements apart, ld >= E):
+ *   an expert is eligible if its logit is greater than -inf; a logit of -inf
+ *   or NaN switches the expert off for this token, +inf counts as the largest
+ *   finite value;
+ *   s_e = 1 / (1 + exp(-l_e)), or softmax of l over the eligible experts;
+ *   c_e = s_e + bias[e] (bias: fp32 [E], finite, or NULL: 0);
+ *   with G > 1, the top_groups groups of largest group value (equal ones: the
+ *   lower group) stay, the other groups' experts are not picked;
+ *   the picks are the k largest c of the eligible experts left, in descending
+ *   order, equal values resolved to the lower id;
+ *   gate_j = scale * s_j, or with renorm scale * s_j / (sum of the picks' s).
+ * topk_idx (int32 [T][k]) and topk_gate (fp32 [T][k]) are written whole; a
+ * token with fewer than k experts to pick has id -1 and gate 0 in the places
+ * behind its picks (mok_build_schedule and the fused layer pass over them).
+ * The order is that of c and of the group values in fp64 (two that differ by
+ * less than 2^-48 of them, and not by nothing, may come in either order).
+ * load (int32 [E], or NULL): the number of tokens that picked each expert is
+ * added to it. */
+mok_status mok_route_scored(const mok_router_desc* router, const void* logits, int32_t logits_type,
+                            int64_t ld, const float* bias, int32_t T, int32_t* topk_idx,
+                            float* topk_gate, int32_t* load, hipStream_t stream);
+
+/* Backward of mok_route_scored: from dgate (fp32 [T][k], the gradient of the
+ * gates; entries of id -1 are not read into the result) the gradient of the
+ * logits, dlogits (logits_type, rows ldd elements apart, ldd >= E), all E
+ * values of every row written.  The picks topk_idx are constants, the bias
+ * has no gradient, and the sums are fp32.  With u_j the pick's share
+ * gate_j / scale, w_j = scale * dgate_j and D = sum_i w_i u_i:
+ *   sigmoid, renorm:  dl_j = u_j (1 - s_j) (w_j - D)
+ *   sigmoid:          dl_j = s_j (1 - s_j) w_j
+ *   softmax, renorm:  dl_j = u_j (w_j - D)
+ *   softmax:          dl_e = s_e ([e picked] w_e - D), for every expert
+ * An id outside [0, E), or of an expert that is not eligible, counts as -1; an
+ * id that occurs twice in a row gets the sum of both.  logits is the forward's
+ * input; dlogits must not overlap it. */
+mok_status mok_route_scored_backward(const mok_router_desc* router, const void* logits,
+                                     int32_t logits_type, int64_t ld, int32_t T,
+                                     const int32_t* topk_idx, const float* dgate, void* dlogits,
+                                     int64_t ldd, hipStream_t stream);
+
+/* Update of the balance bias from the experts' load, for n_layers layers at
+ * once (load: int32 [n_layers][E], not negative; bias: fp32 [n_layers][E]):
+ *   bias[l][e] += rate * sign(sum_i load[l][i] - E * load[l][e])
+ * (the sign from 64-bit integers), so that experts below the mean load are
+ * picked more often.  clear_load != 0: load is zero afterwards.  E up to
+ * 65536. */
+mok_status mok_route_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate,
+                                 float* bias, int32_t clear_load, hipStream_t stream);
+
 /* Bytes of scratch mok_build_schedule needs. */
 size_t mok_schedule_workspace_size(int64_t T, int32_t k, int32_t n_local);
 
@@ -537,6 +609,75 @@ mok_status mok_dispatch_backward(const void* dx_slots, int32_t rows,
                                  int32_t k, int32_t H, const mok_tokens* dx, int32_t* dev_status,
                                  hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * AdamW over many tensors at once (the step that follows the weight gradients
+ * above).  Per element, with g = grad * grad_scale and t the step:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr lr_scale weight_decay)
+ *       - lr lr_scale / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32 (the factors of lr and beta formed in fp64).
+ * ------------------------------------------------------------------------ */
+
+/* States of a tensor.  MOK_STATE_MXFP8: m, and r = sqrt(v) in the place of v,
+ * as E4M3 codes (u8) with one E8M0 scale per 32 consecutive elements (the last
+ * block may be shorter): the smallest scale 2^E, -127 <= E <= 127, with which
+ * the block's largest magnitude is at most 448 (not the MX rule of the token
+ * operands, which lets it saturate: a state is read and written again every
+ * step).  Codes are rounded to one of the two neighbours at random, so that
+ * the mean of m and of r^2 is kept: a step moves a state by a fraction of a
+ * quantum, which rounding to nearest would lose every time.  The random bits
+ * of element i of tensor number j are h = H(i_lo + (i_hi * 0x6A09E667) +
+ * H(H(seed + 0x9E3779B1 t) + j)), 32-bit arithmetic, i_lo and i_hi the halves
+ * of i, H(x): x = (x ^ x >> 16) * 0x9E3779B1; x = (x ^ x >> 15) * 0xBB67AE85;
+ * x ^ x >> 16.  With u(b) = (b + 0.5) / 65536: |m| goes up if its place between
+ * the neighbours is at least 1 - u(h & 0xffff), r if r^2's place between their
+ * squares is above u(h >> 16).  An r > 0 never becomes 0.  A value that is not
+ * finite becomes the code 0x7f (NaN) and does not enter the scale. */
+typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MXFP8 = 1 } mok_state_format;
+
+typedef struct {
+    float* p;            /* parameters, fp32 [n]                                 */
+    void* p_bf16;        /* NULL, or bf16 [n]: the new parameters, rounded       */
+    const void* grad;    /* [n] of grad_type                                     */
+    void* m;             /* fp32 [n], or codes [n]                               */
+    void* v;             /* fp32 [n], or codes [n] of r                          */
+    uint8_t* m_scale;    /* MOK_STATE_MXFP8: [(n + 31) / 32], else not read      */
+    uint8_t* v_scale;
+    int64_t n;           /* elements; 0: the tensor is passed over               */
+    int32_t grad_type;   /* mok_type                                             */
+    int32_t state_format; /* mok_state_format                                    */
+    float lr_scale;      /* factor of lr for this tensor                         */
+    float weight_decay;
+} mok_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps;  /* 0 <= beta < 1                              */
+    double grad_scale;             /* factor of every gradient (unscaling, the
+                                      clipping coefficient)                      */
+    int32_t step;                  /* t, from 1                                  */
+    uint32_t seed;                 /* of the 8-bit states' rounding              */
+} mok_adamw_hyper;
+
+/* The numbers that change from step to step, in device memory: a captured step
+ * reads them anew on every replay. */
+typedef struct {
+    float lr, grad_scale;
+    int32_t step;        /* below 1: as skip                                     */
+    int32_t skip;        /* not 0: nothing is written (a step with overflow)     */
+} mok_adamw_scalars;
+
+/* One step over n_tensors tensors (tensors, hyper: host, read before the call
+ * returns).  scalars: NULL, or device memory (16-byte aligned) whose four
+ * numbers are used in place of hyper's lr, grad_scale and step.  Updates p, m
+ * and v in place.  One launch for up to 44 tensors with n > 0.  No two buffers
+ * that the step writes may overlap; overlapping p are refused
+ * (MOK_ERR_INVALID_ARG).  fp32 pointers must be 4-byte, bf16 pointers 2-byte
+ * aligned; tensors whose pointers are all aligned for 4 elements (16 bytes of
+ * fp32) go faster. */
+mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t n_tensors,
+                          const mok_adamw_hyper* hyper, const mok_adamw_scalars* scalars,
+                          hipStream_t stream);
+
 /* Bytes of workspace mok_moe_forward, mok_moe_forward_routed and
  * mok_moe_forward_batches need for T source tokens per macrobatch and n_macro
  * macrobatches. */
@@ -570,6 +711,21 @@ mok_status mok_moe_forward(const mok_layer_desc* desc, const float* logits, int3
 size_t mok_forward_router_workspace_size(const mok_layer_desc* desc, int32_t T);
 mok_status mok_moe_forward_router(const mok_layer_desc* desc, const void* w_router, int32_t T,
                                   const mok_tokens* x, const void* w_gate_up, const void* w_down,
+                                  const mok_tokens* out, void* ws, size_t ws_bytes,
+                                  hipStream_t stream);
+
+/* The fused layer from logits routed by mok_route_scored (router's n_experts
+ * and top_k equal to desc's; logits, logits_type, ld, bias and load as there):
+ * the scored route also counts the local picks for the schedule, then the
+ * steps of mok_moe_forward.  Results are those of mok_route_scored followed by
+ * mok_moe_forward_routed, bit for bit.  topk_idx / topk_gate: the routing is
+ * written there (int32 / fp32 [T][k], what the backward reads), or into the
+ * workspace if both are NULL. */
+mok_status mok_moe_forward_scored(const mok_layer_desc* desc, const mok_router_desc* router,
+                                  const void* logits, int32_t logits_type, int64_t ld,
+                                  const float* bias, int32_t T, int32_t* topk_idx,
+                                  float* topk_gate, int32_t* load, const mok_tokens* x,
+                                  const void* w_gate_up, const void* w_down,
                                   const mok_tokens* out, void* ws, size_t ws_bytes,
                                   hipStream_t stream);
 

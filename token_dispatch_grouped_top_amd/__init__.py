@@ -34,6 +34,10 @@ MOK_ERR_HIP, MOK_ERR_DEVICE, MOK_ERR_CAPACITY = 4, 5, 6
 MOK_ACT_BF16, MOK_ACT_MXFP8_E4M3 = 0, 1
 MOK_MODE_STREAM, MOK_MODE_PERSISTENT = 0, 1
 MOK_W_BF16, MOK_W_MXFP8_E4M3 = 0, 1
+MOK_TYPE_F32, MOK_TYPE_BF16 = 0, 1
+MOK_SCORE_SOFTMAX, MOK_SCORE_SIGMOID = 0, 1
+MOK_GROUP_MAX, MOK_GROUP_TOP2 = 0, 1
+MOK_STATE_F32, MOK_STATE_MXFP8 = 0, 1
 
 
 class MokError(RuntimeError):
@@ -53,10 +57,35 @@ class mok_tokens(C.Structure):
     _fields_ = [("part_ptr", C.c_void_p), ("n_partitions", C.c_int32), ("part_rows", C.c_int32)]
 
 
+class mok_router_desc(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in (
+        "n_experts", "top_k", "score", "n_groups", "top_groups", "group_rule", "renorm")] + [
+        ("scale", C.c_float)]
+
+
+class mok_adamw_tensor(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("p", "p_bf16", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", C.c_int64), ("grad_type", C.c_int32), ("state_format", C.c_int32),
+        ("lr_scale", C.c_float), ("weight_decay", C.c_float)]
+
+
+class mok_adamw_hyper(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("lr", "beta1", "beta2", "eps", "grad_scale")] + [
+        ("step", C.c_int32), ("seed", C.c_uint32)]
+
+
 _P, _I32, _I64, _SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 _DESC, _TOK = C.POINTER(mok_layer_desc), C.POINTER(mok_tokens)
+_RTR = C.POINTER(mok_router_desc)
 _SIGS = {
     "mok_route_topk": (C.c_int, [_P, _I32, _I32, _I32, _P, _P, _P]),
+    "mok_route_scored": (C.c_int, [_RTR, _P, _I32, _I64, _P, _I32, _P, _P, _P, _P]),
+    "mok_route_scored_backward": (C.c_int, [_RTR, _P, _I32, _I64, _I32, _P, _P, _P, _I64, _P]),
+    "mok_route_bias_update": (C.c_int, [_P, _I32, _I32, C.c_float, _P, _I32, _P]),
+    "mok_adamw_step": (C.c_int, [C.POINTER(mok_adamw_tensor), _I32, C.POINTER(mok_adamw_hyper),
+                                 _P, _P]),
+    "mok_moe_forward_scored": (C.c_int, [_DESC, _RTR, _P, _I32, _I64, _P, _I32, _P, _P, _P, _TOK,
+                                         _P, _P, _TOK, _P, _SZ, _P]),
     "mok_route_gemm_workspace_size": (_SZ, [_I32, _I32, _I32]),
     "mok_route_topk_gemm": (C.c_int, [_P, _P, _I32, _I32, _I32, _I32, _P, _SZ, _P, _P, _P]),
     "mok_schedule_workspace_size": (_SZ, [_I64, _I32, _I32]),
@@ -186,6 +215,120 @@ def mok_status_str(status: int) -> str:
 def mok_route_topk(logits, T: int, E: int, k: int, topk_idx, topk_gate, stream=None) -> None:
     _check(_lib.mok_route_topk(_ptr(logits), T, E, k, _ptr(topk_idx), _ptr(topk_gate),
                                _stream(stream)), "mok_route_topk")
+
+
+_TYPES = {torch.float32: MOK_TYPE_F32, torch.bfloat16: MOK_TYPE_BF16}
+
+
+def _buffer(x, name: str, dtypes, n: int) -> int:
+    """Address of a buffer of at least n elements: None, a raw address (not checked), or a dense
+    tensor of one of dtypes on the current GPU."""
+    if x is None or isinstance(x, int):
+        return x or 0
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name}: {x.dtype} where {' or '.join(map(str, dtypes))} is wanted")
+    if not x.is_contiguous() or x.numel() < n:
+        raise ValueError(f"{name}: {tuple(x.shape)} with strides {x.stride()} where {n} dense elements "
+                         "are wanted")
+    return _on_device(x, name)
+
+
+def _on_device(x, name: str) -> int:
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
+    return x.data_ptr()
+
+
+def _rows(x, name: str, T: int, E: int):
+    """(address, mok_type, row stride) of fp32 or bf16 rows, the rows themselves dense."""
+    if x is None:
+        return 0, MOK_TYPE_F32, E
+    if x.dtype not in _TYPES:
+        raise ValueError(f"{name}: {x.dtype} where torch.float32 or torch.bfloat16 is wanted")
+    if x.dim() != 2 or x.shape[0] < T or x.shape[1] != E or (E > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name}: {tuple(x.shape)} with strides {x.stride()} where [{T}][{E}] rows of "
+                         "dense values are wanted")
+    return _on_device(x, name), _TYPES[x.dtype], x.stride(0) if T > 1 else max(x.stride(0), E)
+
+
+def mok_route_scored(router: mok_router_desc, logits, T: int, topk_idx, topk_gate, bias=None,
+                     load=None, stream=None) -> None:
+    E, n = router.n_experts, T * router.top_k
+    at, kind, ld = _rows(logits, "logits", T, E)
+    _check(_lib.mok_route_scored(C.byref(router), at, kind, ld,
+                                 _buffer(bias, "bias", (torch.float32,), E), T,
+                                 _buffer(topk_idx, "topk_idx", (torch.int32,), n),
+                                 _buffer(topk_gate, "topk_gate", (torch.float32,), n),
+                                 _buffer(load, "load", (torch.int32,), E), _stream(stream)),
+           "mok_route_scored")
+
+
+def mok_route_scored_backward(router: mok_router_desc, logits, T: int, topk_idx, dgate, dlogits,
+                              stream=None) -> None:
+    E, n = router.n_experts, T * router.top_k
+    at, kind, ld = _rows(logits, "logits", T, E)
+    to, kind_to, ldd = _rows(dlogits, "dlogits", T, E)
+    if kind_to != kind:
+        raise ValueError(f"dlogits: {dlogits.dtype} where the logits are {logits.dtype}")
+    _check(_lib.mok_route_scored_backward(C.byref(router), at, kind, ld, T,
+                                          _buffer(topk_idx, "topk_idx", (torch.int32,), n),
+                                          _buffer(dgate, "dgate", (torch.float32,), n), to, ldd,
+                                          _stream(stream)), "mok_route_scored_backward")
+
+
+def mok_route_bias_update(load, n_layers: int, E: int, rate: float, bias, clear_load: int = 0,
+                          stream=None) -> None:
+    _check(_lib.mok_route_bias_update(_buffer(load, "load", (torch.int32,), n_layers * E), n_layers,
+                                      E, rate, _buffer(bias, "bias", (torch.float32,), n_layers * E),
+                                      clear_load, _stream(stream)), "mok_route_bias_update")
+
+
+class AdamwTensors:
+    """Tensors of an AdamW step (a host array of ``mok_adamw_tensor`` plus what keeps them alive).
+
+    One dict per tensor: ``p`` (fp32), ``grad`` (fp32 or bf16), ``m`` and ``v`` (fp32, or uint8
+    codes beside ``m_scale`` and ``v_scale``, uint8), and optionally ``p_bf16``, ``lr_scale`` (1)
+    and ``weight_decay`` (0).  Dense tensors of the same number of elements on one GPU.  Built
+    once for a program's buffers.
+    """
+
+    def __init__(self, tensors: Sequence[dict]):
+        self.tensors = [dict(t) for t in tensors]
+        self.c = (mok_adamw_tensor * len(self.tensors))()
+        f32, u8 = (torch.float32,), (torch.uint8,)
+        for c, t in zip(self.c, self.tensors):
+            n = t["p"].numel()
+            coded = t["m"].dtype == torch.uint8
+            for name, kinds, size in (("p", f32, n), ("grad", tuple(_TYPES), n),
+                                      ("m", u8 if coded else f32, n), ("v", u8 if coded else f32, n),
+                                      ("p_bf16", (torch.bfloat16,), n),
+                                      ("m_scale", u8, (n + 31) // 32), ("v_scale", u8, (n + 31) // 32)):
+                x = t.get(name)
+                if x is None and (name == "p_bf16" or (name.endswith("scale") and not coded)):
+                    continue
+                if x is None:
+                    raise ValueError(f"{name}: missing")
+                address = _buffer(x, name, kinds, size)
+                if x.numel() != size:
+                    raise ValueError(f"{name}: {x.numel()} elements where {size} are wanted")
+                setattr(c, name, address)
+            c.n, c.grad_type = n, _TYPES[t["grad"].dtype]
+            c.state_format = MOK_STATE_MXFP8 if coded else MOK_STATE_F32
+            c.lr_scale, c.weight_decay = t.get("lr_scale", 1.0), t.get("weight_decay", 0.0)
+
+
+def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float, eps: float,
+                   step: int, grad_scale: float = 1.0, seed: int = 0, scalars=None,
+                   stream=None) -> None:
+    """scalars: None, or 16 bytes on the GPU as a ``mok_adamw_scalars`` (lr and grad_scale fp32,
+    step and skip int32)."""
+    if scalars is not None and not isinstance(scalars, int):
+        if scalars.numel() * scalars.element_size() != 16 or not scalars.is_contiguous():
+            raise ValueError("scalars: 16 dense bytes are wanted")
+        scalars = _on_device(scalars, "scalars")
+    h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
+    _check(_lib.mok_adamw_step(tensors.c, len(tensors.c), C.byref(h), scalars or 0,
+                               _stream(stream)), "mok_adamw_step")
 
 
 def mok_route_gemm_workspace_size(T: int, E: int, H: int) -> int:
@@ -342,6 +485,22 @@ def mok_moe_forward(desc: mok_layer_desc, logits, T: int, x: Tokens, w_gate_up, 
 
 def mok_forward_router_workspace_size(desc: mok_layer_desc, T: int) -> int:
     return int(_lib.mok_forward_router_workspace_size(C.byref(desc), T))
+
+
+def mok_moe_forward_scored(desc: mok_layer_desc, router: mok_router_desc, logits, T: int, x: Tokens,
+                           w_gate_up, w_down, out: Tokens, ws, bias=None, topk_idx=None,
+                           topk_gate=None, load=None, ws_bytes: Optional[int] = None,
+                           stream=None) -> None:
+    E, n = router.n_experts, T * router.top_k
+    at, kind, ld = _rows(logits, "logits", T, E)
+    _check(_lib.mok_moe_forward_scored(C.byref(desc), C.byref(router), at, kind, ld,
+                                       _buffer(bias, "bias", (torch.float32,), E), T,
+                                       _buffer(topk_idx, "topk_idx", (torch.int32,), n),
+                                       _buffer(topk_gate, "topk_gate", (torch.float32,), n),
+                                       _buffer(load, "load", (torch.int32,), E), C.byref(x.c),
+                                       _ptr(w_gate_up), _ptr(w_down), C.byref(out.c), _ptr(ws),
+                                       _ws_bytes(ws, ws_bytes), _stream(stream)),
+           "mok_moe_forward_scored")
 
 
 def mok_moe_forward_router(desc: mok_layer_desc, w_router, T: int, x: Tokens, w_gate_up, w_down,

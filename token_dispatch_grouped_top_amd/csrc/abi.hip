@@ -1,10 +1,14 @@
 // abi.hip -- the extern "C" entry points of libmok: argument checks,
 // workspace carving and the stream-ordered orchestration of the fused layer.
-// The kernels live in route.hip, schedule.hip, movers.hip and gemm.hip; the
-// persistent pipeline in persistent.hip.
+// The kernels live in route.hip, route_scored.hip, schedule.hip, movers.hip,
+// gemm.hip, wgrad.hip and adamw.hip; the persistent pipeline in persistent.hip.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
+#include <new>
+#include <utility>
+#include <vector>
 
 #include "mok_internal.h"
 #include "persistent.h"
@@ -168,6 +172,30 @@ bool make_plan(const mok_layer_desc* d, int32_t T, int32_t n_macro, Plan& p) {
 template <class T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off); }
 
+bool router_ok(const mok_router_desc* r) {
+  if (!r || r->n_experts < 1 || r->n_experts > 4096 || r->top_k < 1 || r->top_k > 32) return false;
+  if (r->n_groups < 1 || r->n_groups > 64 || r->n_experts % r->n_groups != 0) return false;
+  if (r->top_groups < 1 || r->top_groups > r->n_groups) return false;
+  if (r->top_k > r->top_groups * (r->n_experts / r->n_groups)) return false;
+  if (r->score != MOK_SCORE_SOFTMAX && r->score != MOK_SCORE_SIGMOID) return false;
+  if (r->group_rule != MOK_GROUP_MAX && r->group_rule != MOK_GROUP_TOP2) return false;
+  if (r->renorm != 0 && r->renorm != 1) return false;
+  return std::isfinite(r->scale);
+}
+
+// Groups that cannot shut an expert out are left out (top_groups = n_groups).
+RouterArgs router_args(const mok_router_desc* r) {
+  RouterArgs a{};
+  a.E = r->n_experts; a.k = r->top_k;
+  a.G = r->top_groups < r->n_groups ? r->n_groups : 1;
+  a.gsize = a.E / a.G; a.top_groups = a.G > 1 ? r->top_groups : 1;
+  a.sigmoid = r->score == MOK_SCORE_SIGMOID; a.top2 = r->group_rule == MOK_GROUP_TOP2;
+  a.renorm = r->renorm; a.scale = r->scale;
+  return a;
+}
+
+bool type_ok(int32_t t) { return t == MOK_TYPE_F32 || t == MOK_TYPE_BF16; }
+
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
 mok_status hip_status(hipError_t e) {
@@ -201,6 +229,79 @@ mok_status mok_route_topk(const float* logits, int32_t T, int32_t E, int32_t k, 
   if (T < 0 || E < 1 || E > 4096 || k < 1 || k > 32 || k > E) return MOK_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_idx || !topk_gate)) return MOK_ERR_INVALID_ARG;
   return hip_status(launch_route_topk(logits, T, E, k, topk_idx, topk_gate, stream));
+}
+
+mok_status mok_route_scored(const mok_router_desc* router, const void* logits, int32_t logits_type,
+                            int64_t ld, const float* bias, int32_t T, int32_t* topk_idx,
+                            float* topk_gate, int32_t* load, hipStream_t stream) {
+  if (!router_ok(router) || !type_ok(logits_type) || T < 0 || ld < router->n_experts)
+    return MOK_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_idx || !topk_gate)) return MOK_ERR_INVALID_ARG;
+  return hip_status(launch_route_scored(router_args(router), logits, logits_type == MOK_TYPE_BF16,
+                                        ld, bias, T, topk_idx, topk_gate, load, RouteCount{},
+                                        stream));
+}
+
+mok_status mok_route_scored_backward(const mok_router_desc* router, const void* logits,
+                                     int32_t logits_type, int64_t ld, int32_t T,
+                                     const int32_t* topk_idx, const float* dgate, void* dlogits,
+                                     int64_t ldd, hipStream_t stream) {
+  if (!router_ok(router) || !type_ok(logits_type) || T < 0 || ld < router->n_experts ||
+      ldd < router->n_experts)
+    return MOK_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_idx || !dgate || !dlogits)) return MOK_ERR_INVALID_ARG;
+  return hip_status(launch_route_scored_bwd(router_args(router), logits,
+                                            logits_type == MOK_TYPE_BF16, ld, T, topk_idx, dgate,
+                                            dlogits, ldd, stream));
+}
+
+mok_status mok_route_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate,
+                                 float* bias, int32_t clear_load, hipStream_t stream) {
+  if (n_layers < 0 || E < 1 || E > 65536 || !std::isfinite(rate)) return MOK_ERR_INVALID_ARG;
+  if (clear_load != 0 && clear_load != 1) return MOK_ERR_INVALID_ARG;
+  if (n_layers > 0 && (!load || !bias)) return MOK_ERR_INVALID_ARG;
+  return hip_status(launch_bias_update(load, n_layers, E, rate, bias, clear_load != 0, stream));
+}
+
+mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t n_tensors,
+                          const mok_adamw_hyper* hyper, const mok_adamw_scalars* scalars,
+                          hipStream_t stream) {
+  if (n_tensors < 0 || !hyper || (n_tensors > 0 && !tensors)) return MOK_ERR_INVALID_ARG;
+  const mok_adamw_hyper& h = *hyper;
+  if (!std::isfinite(h.lr) || !std::isfinite(h.eps) || h.eps < 0.0 || !std::isfinite(h.grad_scale) ||
+      !(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0))
+    return MOK_ERR_INVALID_ARG;
+  if (!scalars && h.step < 1) return MOK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(scalars) % 16 != 0) return MOK_ERR_INVALID_ARG;
+  try {
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // [begin, end) of every p
+    spans.reserve(n_tensors);
+    for (int32_t i = 0; i < n_tensors; ++i) {
+      const mok_adamw_tensor& x = tensors[i];
+      if (x.n < 0 || !type_ok(x.grad_type) || !std::isfinite(x.lr_scale) ||
+          !std::isfinite(x.weight_decay))
+        return MOK_ERR_INVALID_ARG;
+      if (x.state_format != MOK_STATE_F32 && x.state_format != MOK_STATE_MXFP8)
+        return MOK_ERR_INVALID_ARG;
+      if (x.n == 0) continue;
+      if (x.n > adamw_max_elements()) return MOK_ERR_UNSUPPORTED;
+      const bool mx = x.state_format == MOK_STATE_MXFP8;
+      if (!x.p || !x.grad || !x.m || !x.v || (mx && (!x.m_scale || !x.v_scale)))
+        return MOK_ERR_INVALID_ARG;
+      auto odd = [](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a != 0; };
+      if (odd(x.p, 4) || odd(x.p_bf16, 2) || odd(x.grad, x.grad_type == MOK_TYPE_BF16 ? 2 : 4) ||
+          (!mx && (odd(x.m, 4) || odd(x.v, 4))))
+        return MOK_ERR_INVALID_ARG;
+      const uintptr_t at = reinterpret_cast<uintptr_t>(x.p);
+      spans.emplace_back(at, at + static_cast<uintptr_t>(x.n) * 4);
+    }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+      if (spans[i].first < spans[i - 1].second) return MOK_ERR_INVALID_ARG;
+  } catch (const std::bad_alloc&) {
+    return MOK_ERR_UNSUPPORTED;
+  }
+  return hip_status(launch_adamw(tensors, n_tensors, h, scalars, stream));
 }
 
 size_t mok_route_gemm_workspace_size(int32_t T, int32_t E, int32_t H) {
@@ -791,21 +892,35 @@ int32_t mok_forward_minibatch(const mok_layer_desc* desc, int32_t T) {
 namespace mok {
 namespace {
 
+// Scores and routing buffers of the scored form of the fused layer.
+struct ScoredRoute {
+  RouterArgs router;
+  const void* logits;
+  bool bf16;
+  int64_t ld;
+  const float* bias;
+  int32_t* idx;               // null: the workspace's
+  float* gate;
+  int32_t* load;
+};
+
 // The fused layer.  logits non-null (then n_macro = 1): the routing of the T
 // tokens is computed here, from fp32 logits [T][n_experts], into the
 // workspace; w_router non-null (then n_macro = 1): from the router GEMM of
 // the tokens' rows x with the bf16 router rows w_router [n_experts][H], its
-// per-split partial sums in the workspace past the plan's bytes; otherwise
+// per-split partial sums in the workspace past the plan's bytes; scored
+// non-null (then n_macro = 1): by the scored route; otherwise
 // topk_idx / topk_gate hold each macrobatch's routing.
 mok_status forward_impl(const mok_layer_desc* desc, int32_t n_macro, const float* logits,
                         const void* w_router, const int32_t* const* topk_idx,
                         const float* const* topk_gate, int32_t T, const mok_tokens* x,
                         const void* w_gate_up, const void* w_down, const mok_tokens* out,
-                        void* ws, size_t ws_bytes, hipStream_t stream) {
+                        void* ws, size_t ws_bytes, hipStream_t stream,
+                        const ScoredRoute* scored = nullptr) {
   if (!desc_ok(desc) || n_macro < 1 || T < 0 || !tokens_ok(x, T) || !w_gate_up || !w_down ||
       !out || !ws || !weights_ok(desc))
     return MOK_ERR_INVALID_ARG;
-  const bool route_here = logits || w_router;
+  const bool route_here = logits || w_router || scored;
   if (route_here ? (n_macro != 1 || desc->n_experts > 4096)
                  : (!topk_idx || !topk_gate))
     return MOK_ERR_INVALID_ARG;
@@ -836,6 +951,10 @@ mok_status forward_impl(const mok_layer_desc* desc, int32_t n_macro, const float
   split.n_cus = n_cus;
   int32_t* route_idx = at<int32_t>(ws, p.off_route_idx);
   float* route_gate = at<float>(ws, p.off_route_gate);
+  if (scored && scored->idx) {
+    route_idx = scored->idx;
+    route_gate = scored->gate;
+  }
 
   MacroBuffers mb[64];
   const int nm_buf = n_macro < 64 ? n_macro : 64;
@@ -861,11 +980,19 @@ mok_status forward_impl(const mok_layer_desc* desc, int32_t n_macro, const float
                                  d.top_k, at<float>(ws, p.total), route_idx, route_gate, rc, stream);
     if (err != hipSuccess) return hip_status(err);
   }
+  if (scored && T > 0) {     // the scored route, counting the local picks as it goes
+    RouteCount rc;
+    rc.base = d.expert_base; rc.n_local = d.n_local; rc.blk_counts = sw.blk_counts; rc.nblk = sw.nblk;
+    err = launch_route_scored(scored->router, scored->logits, scored->bf16, scored->ld,
+                              scored->bias, T, route_idx, route_gate, scored->load, rc, stream);
+    if (err != hipSuccess) return hip_status(err);
+  }
   for (int m = 0; m < n_macro; ++m) {
     int32_t* idx = route_here ? route_idx : const_cast<int32_t*>(T > 0 ? topk_idx[m] : nullptr);
     err = launch_route_schedule(logits, d.n_experts, route_gate, idx, T, d.top_k, d.expert_base,
                                 d.n_local, mb[m].counts, mb[m].offsets, mb[m].soa, mb[m].aos, sw,
-                                p.M, p.nwin, mb[m].win, p.cap, status, stream, w_router != nullptr);
+                                p.M, p.nwin, mb[m].win, p.cap, status, stream,
+                                w_router != nullptr || scored != nullptr);
     if (err != hipSuccess) return hip_status(err);
   }
 
@@ -968,6 +1095,23 @@ mok_status mok_moe_forward_router(const mok_layer_desc* desc, const void* w_rout
   static const float kNoLogits = 0.0f;     // T = 0: no route at all
   return mok::forward_impl(desc, 1, T > 0 ? nullptr : &kNoLogits, T > 0 ? w_router : nullptr,
                            nullptr, nullptr, T, x, w_gate_up, w_down, out, ws, ws_bytes, stream);
+}
+
+mok_status mok_moe_forward_scored(const mok_layer_desc* desc, const mok_router_desc* router,
+                                  const void* logits, int32_t logits_type, int64_t ld,
+                                  const float* bias, int32_t T, int32_t* topk_idx,
+                                  float* topk_gate, int32_t* load, const mok_tokens* x,
+                                  const void* w_gate_up, const void* w_down,
+                                  const mok_tokens* out, void* ws, size_t ws_bytes,
+                                  hipStream_t stream) {
+  if (!desc || !router_ok(router) || router->n_experts != desc->n_experts ||
+      router->top_k != desc->top_k || !type_ok(logits_type) || ld < router->n_experts ||
+      (T > 0 && !logits) || !topk_idx != !topk_gate)
+    return MOK_ERR_INVALID_ARG;
+  const mok::ScoredRoute sr{router_args(router), logits, logits_type == MOK_TYPE_BF16, ld, bias,
+                            topk_idx, topk_gate, load};
+  return mok::forward_impl(desc, 1, nullptr, nullptr, nullptr, nullptr, T, x, w_gate_up, w_down,
+                           out, ws, ws_bytes, stream, &sr);
 }
 
 mok_status mok_tune_forward(const mok_layer_desc* desc, const int32_t* minibatch,

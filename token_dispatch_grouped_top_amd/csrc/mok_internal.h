@@ -136,6 +136,27 @@ hipError_t launch_route_topk_gemm(const uint16_t* x, void* const* x_parts, int32
 hipError_t launch_route_topk(const float* logits, int32_t T, int32_t E, int32_t k,
                              int32_t* idx, float* gate, hipStream_t s);
 
+// Scored route, its backward and the bias update (mok_router_desc, checked).
+struct RouterArgs {
+  int32_t E, k, G, gsize, top_groups;
+  int32_t sigmoid, top2, renorm;
+  float scale;
+};
+hipError_t launch_route_scored(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
+                               const float* bias, int32_t T, int32_t* idx, float* gate,
+                               int32_t* load, const RouteCount& rc, hipStream_t s);
+hipError_t launch_route_scored_bwd(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
+                                   int32_t T, const int32_t* idx, const float* dgate,
+                                   void* dlogits, int64_t ldd, hipStream_t s);
+hipError_t launch_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate, float* bias,
+                              bool clear_load, hipStream_t s);
+
+// AdamW over a host list of tensors (checked; none above adamw_max_elements).
+constexpr int kAdamwMaxTensors = 44;   // of one launch
+int64_t adamw_max_elements();
+hipError_t launch_adamw(const mok_adamw_tensor* tensors, int32_t n_tensors,
+                        const mok_adamw_hyper& h, const mok_adamw_scalars* scalars, hipStream_t s);
+
 // The schedule counts assignments in chunks of kSchedChunk (a = t*k + j):
 // blk_counts[e][c] = local assignments to expert e in chunk c.
 constexpr int kSchedChunk = 2048;
