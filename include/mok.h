@@ -187,8 +187,10 @@ typedef struct {
  * topk_idx (int32 [T][k]) and topk_gate (fp32 [T][k]) are written whole; a
  * token with fewer than k experts to pick has id -1 and gate 0 in the places
  * behind its picks (mok_build_schedule and the fused layer pass over them).
- * The order is that of c and of the group values in fp64 (two that differ by
- * less than 2^-48 of them, and not by nothing, may come in either order).
+ * The order is that of c (without a bias: of the logits, which is the same)
+ * and of the group values, evaluated in fp64 where fp32 cannot tell; two that
+ * differ by less than 2^-48 of them, and not by nothing, may come in either
+ * order.
  * load (int32 [E], or NULL): the number of tokens that picked each expert is
  * added to it. */
 mok_status mok_route_scored(const mok_router_desc* router, const void* logits, int32_t logits_type,

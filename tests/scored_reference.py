@@ -53,7 +53,8 @@ def route_and_gaps(logits, score, k, bias=None, G=1, top_groups=1, top2=False, r
     l = clean(logits)
     T, E = l.shape
     s = scores(l, score)
-    c = np.where(l > -np.inf, s + (0.0 if bias is None else np.asarray(bias, np.float64)), -np.inf)
+    # without a bias the scores' order is the logits'
+    c = l.copy() if bias is None else np.where(l > -np.inf, s + np.asarray(bias, np.float64), -np.inf)
     b = np.zeros(E) if bias is None else np.asarray(bias, np.float64)
     gaps = np.full(T, np.inf)
     if top_groups < G:
@@ -64,6 +65,8 @@ def route_and_gaps(logits, score, k, bias=None, G=1, top_groups=1, top2=False, r
                 order = np.argsort(-rows[g], kind="stable")[:2]
                 v = rows[g][order]
                 two = top2 and len(v) > 1 and v[1] > -np.inf
+                if top2 and bias is None:
+                    v = np.where(v > -np.inf, s[t, g * (E // G) + order], -np.inf)
                 value.append(v[0] + v[1] if two else v[0])
                 ids = g * (E // G) + order[:2 if two else 1]
                 inputs.append(tuple((l[t, e], b[e]) for e in ids))

@@ -103,6 +103,32 @@ def test_route_matches_reference(E, k, G, top_groups, top2, score):
                 assert np.array_equal(load.cpu().numpy(), rl + 5)
 
 
+@pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
+@pytest.mark.parametrize("E,k,G,top_groups,top2", [
+    (8, 2, 1, 1, False), (3, 3, 1, 1, False), (160, 6, 8, 3, False), (256, 8, 8, 4, True), (384, 8, 1, 1, False),
+    (65, 4, 5, 2, True), (512, 14, 16, 5, True), (201, 7, 3, 2, True), (96, 9, 12, 2, False), (130, 5, 2, 1, True)])
+def test_route_of_many_tokens(E, k, G, top_groups, top2, score):
+    """Four tokens share a wave."""
+    rng = np.random.default_rng(E * 100 + k + score + 7)
+    for case, kind in enumerate(("normal", "ties", "masks", "extreme", "normal", "extreme")):
+        T = 2049 + 7 * case
+        dtype = (torch.float32, torch.bfloat16)[case % 2]
+        renorm, scale, pad = case in (0, 2, 5), (1.0, 2.5)[case % 2], (0, 5, 8)[case % 3]
+        print(f"[route] E={E} k={k} G={G} score={score} {kind} {dtype} T={T}", flush=True)
+        x = _tensor(_logits(rng, T, E, kind), dtype, pad)
+        b = torch.from_numpy(rng.normal(size=E) * 0.1).float().cuda() if case < 4 else None
+        idx = torch.full((T, k), 77, dtype=torch.int32, device="cuda")
+        gate = torch.full((T, k), float("nan"), device="cuda")
+        load = torch.zeros(E, dtype=torch.int32, device="cuda")
+        mok.mok_route_scored(_router(E, k, score, G, top_groups, top2, renorm, scale), x, T, idx, gate, bias=b, load=load)
+        lv = x.double().cpu().numpy()
+        ri, rg, rl = ref.route(lv, score, k, None if b is None else b.cpu().numpy(), G, top_groups, top2, renorm, scale)
+        assert np.array_equal(idx.cpu().numpy(), ri), (kind, dtype)
+        err = np.abs(gate.cpu().numpy().astype(np.float64) - rg)
+        assert np.all(err <= _gate_bar(lv, rg)), (kind, dtype, err.max())
+        assert np.array_equal(load.cpu().numpy(), rl)
+
+
 def test_route_tells_close_scores_apart():
     """Scores that fp32 cannot order: neighbours of one fp32 step in the logits, a bias that brings two scores
     within 2^-40 of each other, and groups whose sums differ in the last bits."""
@@ -114,19 +140,22 @@ def test_route_tells_close_scores_apart():
         l[t] = (l[t].view(np.int32) + rng.permutation(E).astype(np.int32)).view(np.float32)
     for score in (ref.SOFTMAX, ref.SIGMOID):
         for G, tg in ((1, 1), (8, 3)):
-            x = torch.from_numpy(l).cuda()
+            x = torch.from_numpy(np.tile(l, (9, 1))).cuda()      # the rows again: enough for four to a wave
             for bias in (np.zeros(E), rng.integers(-4, 5, E) * 2.0 ** -24):
                 b = torch.from_numpy(bias).float().cuda()
-                idx = torch.empty(T, k, dtype=torch.int32, device="cuda")
-                gate = torch.empty(T, k, device="cuda")
-                mok.mok_route_scored(_router(E, k, score, G, tg, True), x, T, idx, gate, bias=b)
+                idx = torch.empty(9 * T, k, dtype=torch.int32, device="cuda")
+                gate = torch.empty(9 * T, k, device="cuda")
+                mok.mok_route_scored(_router(E, k, score, G, tg, True), x, 9 * T, idx, gate, bias=b)
+                few, fewg = torch.empty_like(idx[:T]), torch.empty_like(gate[:T])
+                mok.mok_route_scored(_router(E, k, score, G, tg, True), x[:T], T, few, fewg, bias=b)
                 ri, _, _, gaps = ref.route_and_gaps(l, score, k, bias, G, tg, True)
                 # Two sums of neighbours, such as p(1 + 3d) + p(1 + 4d) and p(1 + 2d) + p(1 + 5d), differ by p d^2
                 # only, and d goes down to 2^-30 here: below fp64.  An evaluation in fp64 has an exponential (one
                 # step), an addition, a division or product and a sum: less than 8 roundings, so two of them agree on
                 # the order of values that are 2^-48 apart and on nothing less.
                 clear = gaps >= 2.0 ** -48
-                assert np.array_equal(idx.cpu().numpy()[clear], ri[clear]), (score, G)
+                for got in (few, *idx.split(T)):
+                    assert np.array_equal(got.cpu().numpy()[clear], ri[clear]), (score, G)
                 assert clear.sum() > 3 * T // 4
 
 

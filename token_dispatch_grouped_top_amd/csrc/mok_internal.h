@@ -141,6 +141,7 @@ struct RouterArgs {
   int32_t E, k, G, gsize, top_groups;
   int32_t sigmoid, top2, renorm;
   float scale;
+  int32_t log_m, chunk, wide, wide_bias;   // set by the launcher: how a row is split over lanes
 };
 hipError_t launch_route_scored(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
                                const float* bias, int32_t T, int32_t* idx, float* gate,

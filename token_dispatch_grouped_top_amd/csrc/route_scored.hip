@@ -2,11 +2,32 @@
 // bias, expert groups, renormalised weights), its backward and the update of
 // the bias.
 //
-// One wave per token.  Lane l holds the logits l, l + 64, ... in registers.
-// Choice values c = s + bias are formed in fp64: the order of two experts is
-// that of their real scores, which fp32 does not tell apart often enough (of
-// 16384 tokens over 256 experts about one has two neighbours in its order
-// within fp32's error).
+// The order of two experts is that of their choice values c = s + bias in
+// fp64, because fp32 does not tell them apart often enough (of 16384 tokens
+// over 256 experts about ten have two neighbours in their order within fp32's
+// error).  An fp64 exponential of every logit costs more than all the rest,
+// so a token's experts go through two steps:
+//   1. fp32 keys (c with an error below kDelta; without a bias the logits
+//      themselves, whose order is the scores') find a value t0 that at least k
+//      experts reach, and the candidates are those with a key of at least
+//      t0 - 2 kDelta: all that could be among the k largest c, seldom more than
+//      k + 1;
+//   2. the candidates, one to a lane, get c in fp64, and each counts the
+//      candidates before it, which is its place among the picks.
+// Groups are ranked by fp32 values; where the values at the border are nearer
+// than their error, the groups' values are formed in fp64 (exact_groups).
+// Where more candidates are left than lanes (many equal logits), the wave takes
+// the plain way (exact_picks): fp64 for every expert and k rounds of argmax.
+// Keys are kept as integers in the floats' order: their reductions over lanes
+// are one DPP instruction a level.
+//
+// Lanes.  A token has kL = 16 or 64 lanes.  Every group of experts gets m
+// neighbouring lanes (the largest power of two with m G <= kL), each a run of
+// `chunk` experts of its group, so that a group's value is a reduction over m
+// lanes, a lane's experts are open or shut together, and experts in lane order
+// are in id order.
+#include <type_traits>
+
 #include "mok_internal.h"
 
 namespace mok {
@@ -15,6 +36,19 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr float kNegInf = -__builtin_inff();
+constexpr double kNegInf64 = -__builtin_inf();
+// Error of an fp32 key: s = 1 / (1 + 2^(-x log2 e)) with one step (2^-23) each
+// of the exponential and the reciprocal and |x| 2^-23 of the exponent, of which
+// s (1 - s) <= 1/4 and |x| s (1 - s) <= 0.23 reach s: below 2^-22 (softmax: the
+// same of e^x <= 1, x e^x <= 0.37, with its sum's reciprocal: below 2^-21); the
+// sum with the bias adds 2^-24 of itself (kRel, doubled).
+constexpr float kDelta = 0x1p-21f;
+constexpr float kRel = 0x1p-23f;
+constexpr float kLog2e = 1.44269504f;
+// Tokens from which four share a wave.
+constexpr int kManyTokens = 2048;
+// Picks up to which each adds to the load by itself.
+constexpr int kDirectPicks = 2048;
 
 template <bool BF16>
 __device__ __forceinline__ float load_logit(const void* __restrict__ p, int64_t i) {
@@ -29,140 +63,540 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l > kNegInf ? fminf(l, 3.402823466e38f) : kNegInf;
 }
 
+// Integers in the floats' order (zeros of either sign alike), and back.
+__device__ __forceinline__ int key_of(float f) {
+  const int b = __builtin_bit_cast(int, f + 0.0f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_key(int k) {
+  return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff));
+}
+constexpr int kNoKey = static_cast<int>(0x807fffff);   // key_of(-inf)
+
 __device__ __forceinline__ bool better(double v, int e, double bv, int be) {
   return v > bv || (v == bv && e < be);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+// ------------------------------------------------- reductions over kL lanes
+// Within a row of 16 lanes by DPP (xor 1, xor 2, i with 7 - i, i with 15 - i:
+// each level's two sides are uniform in themselves); the four rows of a wave
+// through scalars.  Every lane gets the result.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const int2 b = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, make_int2(dpp<CTRL>(b.x), dpp<CTRL>(b.y)));
+}
+constexpr int kX1 = 0xB1, kX2 = 0x4E, kX4 = 0x141, kX8 = 0x140;   // quad_perm, row_half_mirror, row_mirror
+
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
+}
+__device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ double lane_value(double v, int l) {
+  const int2 b = __builtin_bit_cast(int2, v);
+  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(b.x, l), __builtin_amdgcn_readlane(b.y, l)));
 }
 
-// The picks' shares u: lanes below n hold the logits l of the picks (n >= 1),
-// largest first or not; the other lanes get 0.  sigmoid: s / sum s, formed
-// from exp(l) where every s is as small as exp(l) itself (below 2^-60 of 1),
-// so that nothing underflows.  softmax: exp(l - max) / sum.
+template <int kL, class T, class F>
+__device__ __forceinline__ T reduce(T v, F f) {
+  v = f(v, dpp<kX1>(v));
+  v = f(v, dpp<kX2>(v));
+  v = f(v, dpp<kX4>(v));
+  v = f(v, dpp<kX8>(v));
+  if constexpr (kL == 64)
+    v = f(f(lane_value(v, 0), lane_value(v, 16)), f(lane_value(v, 32), lane_value(v, 48)));
+  return v;
+}
+struct MaxI { __device__ __forceinline__ int operator()(int a, int b) const { return a > b ? a : b; } };
+struct MinI { __device__ __forceinline__ int operator()(int a, int b) const { return a < b ? a : b; } };
+struct MaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+struct Add { template <class T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; } };
+
+__device__ __forceinline__ float wave_max(float v) { return reduce<64>(v, MaxF()); }
+__device__ __forceinline__ double wave_sum(double v) { return reduce<64>(v, Add()); }
+
+__device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
+
+// The picks' shares u: `valid` lanes hold the logits l of the picks (one at
+// least in each token that has any); the other lanes get 0.  sigmoid: s / sum
+// s, formed from exp(l) where every s is as small as exp(l) itself (below
+// e^-60), so that nothing underflows.  softmax: exp(l - max) / sum.
+template <int kL>
 __device__ __forceinline__ double share(bool valid, float l, bool sigmoid, double s) {
-  const float lmax = wave_max(valid ? l : kNegInf);
-  double a;
-  if (sigmoid && lmax > -60.0f) a = valid ? s : 0.0;
-  else a = valid ? exp(static_cast<double>(l) - static_cast<double>(lmax)) : 0.0;
-  return a / wave_sum(a);
+  const float lmax = reduce<kL>(valid ? l : kNegInf, MaxF());
+  double a = s;
+  if (!sigmoid || lmax <= -60.0f) a = exp(static_cast<double>(l) - static_cast<double>(lmax));
+  a = valid ? a : 0.0;
+  const double sum = reduce<kL>(a, Add());
+  return valid ? a / sum : 0.0;
 }
 
-template <int VPL, bool BF16>
-__global__ __launch_bounds__(kWaves * kWave)
-void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
-                    const float* __restrict__ bias, int32_t T, int32_t* __restrict__ idx,
-                    float* __restrict__ gate, int32_t* __restrict__ load, RouteCount rc) {
-  extern __shared__ double lds[];           // groups: [waves][E] choice values
-  const int lane = lane_id(), w = threadIdx.x / kWave;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / kWave) + w;
-  if (t >= T) return;
-  const int E = r.E;
-  float l[VPL];
-  double c[VPL];
-  float lmax = kNegInf;
+// One token's row as its lanes see it.
+struct Row {
+  int sl;         // lane within the token
+  int g, part;    // its group, and its run in the group
+  int first, n;   // its experts [first, first + n)
+};
+
+template <int kL>
+__device__ __forceinline__ Row row_of(const RouterArgs& r, int lane) {
+  Row o;
+  o.sl = lane & (kL - 1);
+  o.g = o.sl >> r.log_m;
+  o.part = o.sl & ((1 << r.log_m) - 1);
+  const int from = o.part * r.chunk;
+  o.first = o.g * r.gsize + from;
+  o.n = o.g < r.G && from < r.gsize ? (r.gsize - from < r.chunk ? r.gsize - from : r.chunk) : 0;
+  return o;
+}
+
+// Largest and second largest of the m lanes of each group, in every lane.
+template <class T, class F>
+__device__ __forceinline__ void merge_top2(T& a, T& b, int log_m, F max2) {
+  auto step = [&](T oa, T ob) {
+    const T lo = oa < a ? oa : a;
+    a = max2(a, oa);
+    b = max2(lo, max2(b, ob));
+  };
+  if (log_m > 0) step(dpp<kX1>(a), dpp<kX1>(b));
+  if (log_m > 1) step(dpp<kX2>(a), dpp<kX2>(b));
+  if (log_m > 2) step(dpp<kX4>(a), dpp<kX4>(b));
+  if (log_m > 3) step(dpp<kX8>(a), dpp<kX8>(b));
+  if (log_m > 4) step(__shfl_xor(a, 16), __shfl_xor(b, 16));
+}
+
+// The plain way, for every token of the wave: c in fp64 for every expert, group
+// values in fp64, k rounds of argmax.  Returns the pick of rank sl, or -1.
+template <int kL, int V, bool BF16>
+__device__ __forceinline__ int exact_picks(const RouterArgs& r, const void* __restrict__ logits,
+                                           int64_t at, const float* __restrict__ bias, float top) {
+  const int lane = lane_id();
+  const Row w = row_of<kL>(r, lane);
+  double c[V], sum = 0.0;                  // the logits are read again: registers
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + kWave * i;
-    l[i] = e < E ? clean_logit(load_logit<BF16>(logits, t * ld + e)) : kNegInf;
-    lmax = fmaxf(lmax, l[i]);
+  for (int i = 0; i < V; ++i) {
+    const float l = i < w.n ? clean_logit(load_logit<BF16>(logits, at + w.first + i)) : kNegInf;
+    c[i] = kNegInf64;
+    if (l > kNegInf) {
+      c[i] = static_cast<double>(l);
+      if (bias && !r.sigmoid) sum += exp(c[i] - static_cast<double>(top));
+    }
   }
-  double inv = 1.0;                         // softmax: 1 / sum
-  const double top = static_cast<double>(wave_max(lmax));
-  if (!r.sigmoid) {
-    double sum = 0.0;
+  sum = reduce<kL>(sum, Add());
+  auto score = [&](double x) {             // without a bias exp(x - top): a common factor orders nothing
+    const double s = r.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(top));
+    return bias && !r.sigmoid ? s / sum : s;
+  };
+  if (bias) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (l[i] > kNegInf) sum += exp(static_cast<double>(l[i]) - top);
-    sum = wave_sum(sum);
-    inv = sum > 0.0 ? 1.0 / sum : 0.0;
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane + kWave * i;
-    const double x = static_cast<double>(l[i]);
-    double s = r.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - top) * inv;
-    if (bias && e < E) s += static_cast<double>(bias[e]);
-    c[i] = l[i] > kNegInf ? s : -__builtin_inf();
+    for (int i = 0; i < V; ++i)
+      if (c[i] > kNegInf64) c[i] = score(c[i]) + static_cast<double>(bias[w.first + i]);
   }
   if (r.G > 1) {
-    double* row = lds + w * E;
+    double a = kNegInf64, b = kNegInf64;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + kWave * i < E) row[lane + kWave * i] = c[i];
-    __builtin_amdgcn_wave_barrier();
-    double gv = -__builtin_inf();
-    if (lane < r.G) {
-      double g2 = -__builtin_inf();
-      for (int j = 0; j < r.gsize; ++j) {
-        const double v = row[lane * r.gsize + j];
-        if (v > gv) { g2 = gv; gv = v; }
-        else if (v > g2) g2 = v;
-      }
-      if (r.top2 && g2 > -__builtin_inf()) gv += g2;
+    for (int i = 0; i < V; ++i) {
+      b = c[i] > a ? a : (c[i] > b ? c[i] : b);
+      a = c[i] > a ? c[i] : a;
     }
-    int rank = 0;                           // groups before this one
+    merge_top2(a, b, r.log_m, [](double x, double y) { return x > y ? x : y; });
+    if (r.top2 && !bias) {
+      a = a > kNegInf64 ? score(a) : a;
+      b = b > kNegInf64 ? score(b) : b;
+    }
+    const double gv = r.top2 && b > kNegInf64 ? a + b : a;
+    int rank = 0;
     for (int g = 0; g < r.G; ++g) {
-      const double ov = __shfl(gv, g);
-      rank += g != lane && better(ov, g, gv, lane);
+      const double ov = __shfl(gv, (lane & ~(kL - 1)) + (g << r.log_m));
+      rank += better(ov, g, gv, w.g) ? 1 : 0;
     }
-    const uint64_t open = __ballot(lane < r.G && rank < r.top_groups);
+    if (rank >= r.top_groups) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + kWave * i;
-      if (e < E && !((open >> (e / r.gsize)) & 1ull)) c[i] = -__builtin_inf();
+      for (int i = 0; i < V; ++i) c[i] = kNegInf64;
     }
   }
-  int mine_e = -1;
-  uint64_t taken = 0;
+  int mine = -1;
   for (int j = 0; j < r.k; ++j) {
-    double bv = -__builtin_inf();
+    double bv = kNegInf64;
     int be = 0x7fffffff;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = lane + kWave * i;
-      if (!((taken >> i) & 1ull) && c[i] > -__builtin_inf() && better(c[i], e, bv, be)) {
-        bv = c[i];
-        be = e;
-      }
-    }
+    for (int i = 0; i < V; ++i)
+      if (c[i] > bv) { bv = c[i]; be = w.first + i; }
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
+    for (int o = 1; o < kL; o <<= 1) {
       const double ov = __shfl_xor(bv, o);
       const int oe = __shfl_xor(be, o);
       if (better(ov, oe, bv, be)) { bv = ov; be = oe; }
     }
-    if (be == 0x7fffffff) break;
-    if ((be & (kWave - 1)) == lane) taken |= 1ull << (be / kWave);
-    if (lane == j) mine_e = be;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (w.first + i == be) c[i] = kNegInf64;
+    if (w.sl == j && bv > kNegInf64) mine = be;
   }
-  const bool valid = mine_e >= 0;
-  const float ml = valid ? clean_logit(load_logit<BF16>(logits, t * ld + mine_e)) : kNegInf;
+  return mine;
+}
+
+// How many lanes of the token's row of 16 hold a larger value (kL = 16).
+template <int R>
+__device__ __forceinline__ int count_before16(double v) {
+  if constexpr (R == 16) return 0;
+  else return (dpp<0x120 + R>(v) > v ? 1 : 0) + count_before16<R + 1>(v);   // row_ror:R
+}
+
+// Groups before this lane's by (value, lane): for the first lane of each group;
+// the other lanes hold kNoKey.  The source of row_ror:R is below lane sl if sl >= R.
+template <int R>
+__device__ __forceinline__ int groups_before16(int rep, int own, int sl) {
+  if constexpr (R == 16) return 0;
+  else return (dpp<0x120 + R>(rep) > own - (sl >= R ? 1 : 0) ? 1 : 0) + groups_before16<R + 1>(rep, own, sl);
+}
+
+// Whether the lane's group is among the top_groups, from values in fp64 of the
+// experts whose keys could be its two largest.  Every lane of the wave calls it.
+template <int kL, int V, bool BF16>
+__device__ __forceinline__ bool exact_groups(const RouterArgs& r, const Row& w, const void* __restrict__ logits,
+                                             int64_t at, const float* __restrict__ bias, float top,
+                                             double inv, const int (&key)[V], int ga, int gb) {
+  const int lane = lane_id();
+  auto score = [&](double x) {
+    return r.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(top)) * inv;
+  };
+  double a = kNegInf64, b = kNegInf64;
+  if (bias) {
+    const float low = of_key(r.top2 && gb > kNoKey ? gb : ga);
+    const int from = key_of(low - 2.0f * (kDelta + kRel * fabsf(low)));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] >= from && key[i] > kNoKey) {
+        const float l = clean_logit(load_logit<BF16>(logits, at + w.first + i));
+        const double c = score(static_cast<double>(l)) + static_cast<double>(bias[w.first + i]);
+        b = c > a ? a : (c > b ? c : b);
+        a = c > a ? c : a;
+      }
+    merge_top2(a, b, r.log_m, [](double x, double y) { return x > y ? x : y; });
+  } else {                       // keys are logits: these are the two
+    if (ga > kNoKey) a = score(static_cast<double>(of_key(ga)));
+    if (gb > kNoKey) b = score(static_cast<double>(of_key(gb)));
+  }
+  const double gv = r.top2 && b > kNegInf64 ? a + b : a;
+  int rank = 0;
+  for (int g = 0; g < r.G; ++g) {
+    const double ov = __shfl(gv, (lane & ~(kL - 1)) + (g << r.log_m));
+    rank += better(ov, g, gv, w.g) ? 1 : 0;
+  }
+  return rank < r.top_groups;
+}
+
+template <int kL, int V, bool BF16>
+__global__ __launch_bounds__(kWaves * kWave)
+void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
+                    const float* __restrict__ bias, int32_t T, int32_t* __restrict__ idx,
+                    float* __restrict__ gate, int32_t* __restrict__ load, RouteCount rc) {
+  constexpr int kTok = kWave / kL;                      // tokens of a wave
+  __shared__ uint16_t slots[kWaves][kTok][kL];
+  const int lane = lane_id(), wave = threadIdx.x / kWave, sub = lane / kL;
+  const Row w = row_of<kL>(r, lane);
+  const int64_t t_mine = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTok + sub;
+  const bool live = t_mine < T;
+  const int64_t t = live ? t_mine : T - 1;              // a wave's spare lanes repeat the last token
+  const int64_t at = t * ld;
+  float l[V];
+  if (r.wide) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      float4 q = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+      if (i < w.n) {
+        if constexpr (BF16) {
+          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + at + w.first + i);
+          q = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                          __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+        } else {
+          q = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + at + w.first + i);
+        }
+      }
+      l[i] = q.x; l[i + 1] = q.y; l[i + 2] = q.z; l[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < w.n ? load_logit<BF16>(logits, at + w.first + i) : kNegInf;
+  }
+  float bv[V];
+  if (bias) {
+    if (r.wide && r.wide_bias) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < w.n) q = *reinterpret_cast<const float4*>(bias + w.first + i);
+        bv[i] = q.x; bv[i + 1] = q.y; bv[i + 2] = q.z; bv[i + 3] = q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) bv[i] = i < w.n ? bias[w.first + i] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = clean_logit(l[i]);
+
+  // softmax: the row's largest logit and its sum (fp64 where the order needs it)
+  float top = 0.0f;
+  double inv = 1.0;
+  if (!r.sigmoid) {
+    float m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+    top = of_key(reduce<kL>(key_of(m), MaxI()));
+    if (bias) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (l[i] > kNegInf) sum += exp(static_cast<double>(l[i]) - static_cast<double>(top));
+      sum = reduce<kL>(sum, Add());
+      inv = sum > 0.0 ? 1.0 / sum : 0.0;
+    } else if (!r.renorm) {
+      // exp(x) = 2^(x log2 e) with the product's rounding error made good
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float x = fmaxf(l[i] - top, -256.0f), y = x * kLog2e;
+        const float more = fmaf(x, kLog2e, -y) + x * 1.92596299e-8f;
+        const float ex = __builtin_amdgcn_exp2f(y);
+        sum += l[i] > kNegInf ? fmaf(ex, more * 0.693147181f, ex) : 0.0f;
+      }
+      sum = reduce<kL>(sum, Add());
+      inv = sum > 0.0f ? 1.0 / static_cast<double>(sum) : 0.0;
+    }
+  }
+  const float inv32 = static_cast<float>(inv);
+  auto sigmoid32 = [](float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
+  };
+  auto softmax32 = [&](float x) { return __builtin_amdgcn_exp2f(kLog2e * (x - top)) * inv32; };
+
+  // keys, and the four largest of the lane's
+  int key[V];
+  if (!bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = key_of(l[i]);
+  } else if (r.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = l[i] > kNegInf ? key_of(sigmoid32(l[i]) + bv[i]) : kNoKey;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = l[i] > kNegInf ? key_of(softmax32(l[i]) + bv[i]) : kNoKey;
+  }
+  auto med3 = [](int lo, int hi, int x) {    // of lo <= hi and x
+    const int y = x > lo ? x : lo;
+    return y < hi ? y : hi;
+  };
+  int a1 = kNoKey, a2 = kNoKey, a3 = kNoKey, a4 = kNoKey;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a4 = med3(a4, a3, key[i]);
+    a3 = med3(a3, a2, key[i]);
+    a2 = med3(a2, a1, key[i]);
+    a1 = key[i] > a1 ? key[i] : a1;
+  }
+
+  bool open = w.n > 0;
+  if (r.G > 1) {
+    int ga = a1, gb = a2;
+    merge_top2(ga, gb, r.log_m, MaxI());
+    const float fa = of_key(ga);
+    float gv = fa, err = bias ? kDelta + kRel * fabsf(fa) : 0.0f;
+    if (r.top2) {
+      float fb = of_key(gb);
+      if (!bias) {               // keys are logits: the sum is of scores
+        gv = ga > kNoKey ? (r.sigmoid ? sigmoid32(fa) : softmax32(fa)) : kNegInf;
+        fb = gb > kNoKey ? (r.sigmoid ? sigmoid32(fb) : softmax32(fb)) : kNegInf;
+      }
+      if (gb > kNoKey) gv += fb;
+      err = 2.0f * kDelta + 2.0f * kRel * (bias ? fabsf(fa) + (gb > kNoKey ? fabsf(fb) : 0.0f) : gv);
+      // without a bias the relative error counts too, below 2^-16 for |x| < 104 (and 2^-120 for
+      // exponentials that leave the normal numbers)
+      if (!bias) err = fminf(err, 0x1p-16f * gv) + 0x1p-120f;
+    }
+    const bool counts = w.g < r.G && ga > kNoKey;
+    const int gk = counts ? key_of(gv) : kNoKey;
+    const int rep = w.part == 0 ? gk : kNoKey;
+    int before = 0;
+    if constexpr (kL == 16) {
+      before = groups_before16<1>(rep, gk, w.sl);
+    } else {
+      for (int g = 0; g < r.G; ++g) {
+        const int o = lane_value(rep, g << r.log_m);
+        before += o > gk || (o == gk && g < w.g) ? 1 : 0;
+      }
+    }
+    // the first lane's verdict, for its group
+    const uint64_t in = __ballot(w.part == 0 && counts && before < r.top_groups);
+    bool chosen = (in >> (lane & ~((1 << r.log_m) - 1))) & 1ull;
+    if (bias || r.top2) {
+      const int last = reduce<kL>(chosen ? key_of(gv - err) : 0x7fffffff, MinI());
+      const int next = reduce<kL>(!chosen && counts ? key_of(gv + err) : kNoKey, MaxI());
+      const bool near = next > kNoKey && next >= last;
+      if (__ballot(near)) {
+        const bool sure = exact_groups<kL, V, BF16>(r, w, logits, at, bias, top, inv, key, ga, gb);
+        chosen = near ? sure : chosen;
+      }
+    }
+    open = open && chosen;
+    if (!open) a1 = a2 = a3 = a4 = kNoKey;
+  }
+
+  // t0: after k rounds of taking the largest heads off, at least k keys were >= it
+  int t0 = kNoKey;
+  for (int j = 0; j < r.k; ++j) {
+    t0 = reduce<kL>(a1, MaxI());
+    const bool off = a1 == t0;
+    a1 = off ? a2 : a1;
+    a2 = off ? a3 : a2;
+    a3 = off ? a4 : a3;
+    a4 = off ? kNoKey : a4;
+  }
+  int thr = t0;
+  if (bias && t0 > kNoKey) {
+    const float f = of_key(t0);
+    thr = key_of(f - 2.0f * (kDelta + kRel * fabsf(f)));
+  }
+  thr = thr > kNoKey ? thr : kNoKey + 1;                // every eligible expert, where k are not there
+  if (!open) thr = 0x7fffffff;
+
+  // candidates, in id order
+  using Bits = typename std::conditional<V <= 32, uint32_t, uint64_t>::type;
+  Bits bits = 0;
+  int have = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (V <= 64) bits |= key[i] >= thr ? Bits{1} << (i & (8 * sizeof(Bits) - 1)) : Bits{0};
+    else have += key[i] >= thr ? 1 : 0;
+  }
+  if (V <= 64) have = __popcll(bits);
+  int slot = have;                                      // inclusive prefix over the token's lanes
+  slot += dpp<0x111>(slot);                             // row_shr:1, 2, 4, 8 (0 from outside)
+  slot += dpp<0x112>(slot);
+  slot += dpp<0x114>(slot);
+  slot += dpp<0x118>(slot);
+  int n_cand;
+  if constexpr (kL == 16) {
+    n_cand = reduce<16>(slot, MaxI());
+  } else {
+    const int r0 = lane_value(slot, 15), r1 = lane_value(slot, 31), r2 = lane_value(slot, 47);
+    const int row = lane >> 4;
+    slot += (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
+    n_cand = lane_value(slot, 63);
+  }
+  slot -= have;
+  uint16_t* mine = slots[wave][sub];
+  if constexpr (V <= 64) {
+    while (bits) {
+      const int i = __ffsll(static_cast<unsigned long long>(bits)) - 1;
+      bits &= bits - 1;
+      if (slot < kL) mine[slot] = static_cast<uint16_t>(w.first + i);
+      ++slot;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] >= thr) {
+        if (slot < kL) mine[slot] = static_cast<uint16_t>(w.first + i);
+        ++slot;
+      }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const bool plain = n_cand > kL;
+
+  // fp64 values of the candidates, one to a lane, and their places
+  int e = -1, place = w.sl;
+  float le = kNegInf;
   double s = 0.0;
-  if (valid)
-    s = r.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(ml)))
-                  : exp(static_cast<double>(ml) - top) * inv;
-  if (r.renorm && __ballot(valid)) s = share(valid, ml, r.sigmoid, s);
-  if (lane < r.k) {
-    idx[t * r.k + lane] = mine_e;
-    gate[t * r.k + lane] = static_cast<float>(static_cast<double>(r.scale) * s);
+  auto score64 = [&]() {
+    le = e >= 0 ? clean_logit(load_logit<BF16>(logits, at + e)) : kNegInf;
+    s = 0.0;
+    if (e >= 0)
+      s = r.sigmoid ? sigmoid64(le) : exp(static_cast<double>(le) - static_cast<double>(top)) * inv;
+  };
+  if (!plain && w.sl < n_cand) e = mine[w.sl];
+  score64();
+  {
+    double v = kNegInf64;
+    if (e >= 0) v = bias ? s + static_cast<double>(bias[e]) : static_cast<double>(le);
+    // equal values in id order, which is lane order: the lane's number in the last bits (the larger
+    // value for the lower lane, of either sign)
+    if (e >= 0) {
+      const uint64_t u = __builtin_bit_cast(uint64_t, v == 0.0 ? 0.0 : v);
+      const uint64_t low = static_cast<uint64_t>((u >> 63) ? w.sl : kL - 1 - w.sl);
+      v = __builtin_bit_cast(double, (u & ~static_cast<uint64_t>(kL - 1)) | low);
+    }
+    if constexpr (kL == 16) {
+      place = count_before16<1>(v);
+    } else {
+      place = 0;
+      const int n = n_cand < kL ? n_cand : kL;
+      for (int j = 0; j < n; ++j) place += lane_value(v, j) > v ? 1 : 0;
+    }
   }
-  if (valid && load)
-    __hip_atomic_fetch_add(load + mine_e, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  // the fused layer's schedule counts
-  const int le = mine_e - rc.base;
-  if (valid && rc.blk_counts && le >= 0 && le < rc.n_local)
-    __hip_atomic_fetch_add(rc.blk_counts + static_cast<int64_t>(le) * rc.nblk +
-                               (t * r.k + lane) / kSchedChunk,
-                           1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (__ballot(plain)) {
+    const int pe = exact_picks<kL, V, BF16>(r, logits, at, bias, top);
+    if (plain) {
+      e = pe;
+      place = w.sl;
+      score64();
+    }
+  }
+  const bool valid = e >= 0 && place < r.k;
+  if (r.renorm) s = share<kL>(valid, le, r.sigmoid, s);
+  if (!live) return;
+  const int64_t to = t * r.k;
+  if (valid) {
+    idx[to + place] = e;
+    gate[to + place] = static_cast<float>(static_cast<double>(r.scale) * s);
+    if (load) __hip_atomic_fetch_add(load + e, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // the fused layer's schedule counts
+    const int local = e - rc.base;
+    if (rc.blk_counts && local >= 0 && local < rc.n_local)
+      __hip_atomic_fetch_add(rc.blk_counts + static_cast<int64_t>(local) * rc.nblk +
+                                 (to + place) / kSchedChunk,
+                             1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  } else if (e < 0 && w.sl < r.k) {           // fewer candidates than k: the places behind them
+    idx[to + w.sl] = -1;
+    gate[to + w.sl] = 0.0f;
+  }
+}
+
+// The load of many picks: a workgroup counts its share in LDS and adds each
+// expert's count once.  (One atomic for each pick costs about 1 ns, all of them
+// on the same few lines: 131072 picks of 256 experts 130 us.)
+constexpr int kLoadThreads = 1024, kLoadPicks = 8 * kLoadThreads;
+
+__global__ __launch_bounds__(kLoadThreads)
+void k_load_count(const int32_t* __restrict__ idx, int64_t n, int32_t E, int32_t* __restrict__ load) {
+  __shared__ int32_t hist[4096];
+  for (int e = threadIdx.x; e < E; e += kLoadThreads) hist[e] = 0;
+  __syncthreads();
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kLoadPicks; i0 < n;
+       i0 += static_cast<int64_t>(gridDim.x) * kLoadPicks) {
+    int e[kLoadPicks / kLoadThreads];
+#pragma unroll
+    for (int j = 0; j < kLoadPicks / kLoadThreads; ++j) {
+      const int64_t i = i0 + j * kLoadThreads + threadIdx.x;
+      e[j] = i < n ? idx[i] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoadPicks / kLoadThreads; ++j)
+      if (e[j] >= 0) atomicAdd(&hist[e[j]], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kLoadThreads)
+    if (hist[e]) __hip_atomic_fetch_add(load + e, hist[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 template <int VPL, bool BF16>
@@ -188,10 +622,8 @@ void k_route_scored_bwd(RouterArgs r, const void* __restrict__ logits, int64_t l
   if (r.sigmoid && valid) s = 1.0 / (1.0 + exp(-x));
   const double not_s = r.sigmoid ? (valid ? 1.0 / (1.0 + exp(x)) : 0.0) : 1.0;
   if (r.renorm) {
-    if (__ballot(valid)) {
-      const double u = share(valid, l, r.sigmoid, s);
-      d = u * not_s * (wg - wave_sum(wg * u));
-    }
+    const double u = share<64>(valid, l, r.sigmoid, s);
+    d = u * not_s * (wg - wave_sum(wg * u));
   } else if (r.sigmoid) {
     d = s * not_s * wg;
   } else {
@@ -260,20 +692,40 @@ void k_bias_update(int32_t* __restrict__ load, int32_t E, float rate, float* __r
   }
 }
 
-template <int VPL>
-hipError_t launch_scored_vpl(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
-                             const float* bias, int32_t T, int32_t* idx, float* gate,
-                             int32_t* load, const RouteCount& rc, hipStream_t s) {
-  const int waves = r.E <= 2048 ? kWaves : 2;   // at most 64 KiB of choice values
-  const dim3 grid((T + waves - 1) / waves), block(waves * kWave);
-  const size_t lds = r.G > 1 ? sizeof(double) * waves * r.E : 0;
+template <int kL, int V>
+hipError_t launch_scored_v(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
+                           const float* bias, int32_t T, int32_t* idx, float* gate, int32_t* load,
+                           const RouteCount& rc, hipStream_t s) {
+  constexpr int kTok = kWaves * (kWave / kL);           // tokens of a workgroup
+  const dim3 grid((T + kTok - 1) / kTok), block(kWaves * kWave);
+  const int64_t picks = static_cast<int64_t>(T) * r.k;
+  int32_t* direct = picks <= kDirectPicks ? load : nullptr;
   if (bf16)
-    hipLaunchKernelGGL((k_route_scored<VPL, true>), grid, block, lds, s, r, logits, ld, bias, T,
-                       idx, gate, load, rc);
+    hipLaunchKernelGGL((k_route_scored<kL, V, true>), grid, block, 0, s, r, logits, ld, bias, T,
+                       idx, gate, direct, rc);
   else
-    hipLaunchKernelGGL((k_route_scored<VPL, false>), grid, block, lds, s, r, logits, ld, bias, T,
-                       idx, gate, load, rc);
-  return hipGetLastError();
+    hipLaunchKernelGGL((k_route_scored<kL, V, false>), grid, block, 0, s, r, logits, ld, bias, T,
+                       idx, gate, direct, rc);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && load && !direct) {
+    const int64_t blocks = (picks + kLoadPicks - 1) / kLoadPicks;
+    hipLaunchKernelGGL(k_load_count, dim3(blocks < 64 ? blocks : 64), dim3(kLoadThreads), 0, s, idx,
+                       picks, r.E, load);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+// The split of a row over kL lanes; false: not possible within max_chunk.
+bool split_row(RouterArgs& r, int kL, int max_chunk) {
+  if (r.G > kL) return false;
+  r.log_m = 0;
+  while ((r.G << (r.log_m + 1)) <= kL) ++r.log_m;
+  const int m = 1 << r.log_m;
+  r.chunk = (r.gsize + m - 1) / m;
+  if (r.chunk % 4 != 0 && r.gsize % 4 == 0 && (r.chunk + 3) / 4 * 4 <= max_chunk)
+    r.chunk = (r.chunk + 3) / 4 * 4;                    // runs of whole 16-byte loads
+  return r.chunk <= max_chunk;
 }
 
 template <int VPL>
@@ -292,18 +744,34 @@ hipError_t launch_bwd_vpl(const RouterArgs& r, const void* logits, bool bf16, in
 
 }  // namespace
 
-hipError_t launch_route_scored(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
+hipError_t launch_route_scored(const RouterArgs& router, const void* logits, bool bf16, int64_t ld,
                                const float* bias, int32_t T, int32_t* idx, float* gate,
                                int32_t* load, const RouteCount& rc, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const int E = r.E;
-  if (E <= 64) return launch_scored_vpl<1>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
-  if (E <= 128) return launch_scored_vpl<2>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
-  if (E <= 256) return launch_scored_vpl<4>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
-  if (E <= 512) return launch_scored_vpl<8>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
-  if (E <= 1024) return launch_scored_vpl<16>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
-  if (E <= 2048) return launch_scored_vpl<32>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
-  return launch_scored_vpl<64>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  RouterArgs r = router;
+  const auto wide = [&]() {
+    const uintptr_t bytes = bf16 ? 8 : 16;
+    r.wide = r.chunk % 4 == 0 && r.gsize % 4 == 0 && ld % 4 == 0 &&
+             reinterpret_cast<uintptr_t>(logits) % bytes == 0;
+    r.wide_bias = reinterpret_cast<uintptr_t>(bias) % 16 == 0;
+  };
+  if (T >= kManyTokens && r.k <= 14 && split_row(r, 16, 32)) {
+    wide();
+    if (r.chunk <= 4) return launch_scored_v<16, 4>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+    if (r.chunk <= 8) return launch_scored_v<16, 8>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+    if (r.chunk <= 12) return launch_scored_v<16, 12>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+    if (r.chunk <= 16) return launch_scored_v<16, 16>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+    if (r.chunk <= 24) return launch_scored_v<16, 24>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+    return launch_scored_v<16, 32>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  }
+  if (!split_row(r, 64, 128)) return hipErrorInvalidValue;
+  wide();
+  if (r.chunk <= 4) return launch_scored_v<64, 4>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  if (r.chunk <= 8) return launch_scored_v<64, 8>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  if (r.chunk <= 16) return launch_scored_v<64, 16>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  if (r.chunk <= 32) return launch_scored_v<64, 32>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  if (r.chunk <= 64) return launch_scored_v<64, 64>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
+  return launch_scored_v<64, 128>(r, logits, bf16, ld, bias, T, idx, gate, load, rc, s);
 }
 
 hipError_t launch_route_scored_bwd(const RouterArgs& r, const void* logits, bool bf16, int64_t ld,
