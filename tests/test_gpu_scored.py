@@ -160,7 +160,8 @@ def test_route_tells_close_scores_apart():
 
 
 @pytest.mark.parametrize("score", [ref.SOFTMAX, ref.SIGMOID])
-@pytest.mark.parametrize("E,k", [(8, 2), (1, 1), (7, 7), (160, 6), (256, 8), (384, 8), (513, 12), (1000, 32), (4096, 3)])
+@pytest.mark.parametrize("E,k", [(8, 2), (1, 1), (7, 7), (50, 16), (100, 5), (160, 6), (256, 8), (384, 8), (513, 12), (1000, 32),
+                                 (2000, 4), (4096, 3)])
 def test_backward_matches_reference(E, k, score):
     rng = np.random.default_rng(E * 10 + k + score)
     case = 0
@@ -168,7 +169,7 @@ def test_backward_matches_reference(E, k, score):
         for dtype in (torch.float32, torch.bfloat16):
             for renorm in (False, True):
                 case += 1
-                T = (1, 3, 70, 129)[case % 4]
+                T = (1, 3, 70, 129, 2051, 2049)[case % 6]      # from 2048 tokens four share a wave
                 scale, pad = (1.0, 2.5)[case % 2], (0, 5, 8)[case % 3]
                 print(f"[bwd] E={E} k={k} score={score} {kind} {dtype} renorm={renorm} T={T}", flush=True)
                 x = _tensor(_logits(rng, T, E, kind), dtype, pad)

@@ -173,7 +173,9 @@ def _ptr(x) -> int:
 
 def _stream(s) -> int:
     if s is None:
-        import torch
+        # the handle alone: building torch's Stream object takes 2.7 us, more than a small launch
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
@@ -234,7 +236,8 @@ def _buffer(x, name: str, dtypes, n: int) -> int:
 
 
 def _on_device(x, name: str) -> int:
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+    device = x.get_device()
+    if device < 0 or device != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
     return x.data_ptr()
 

@@ -73,6 +73,15 @@ __device__ __forceinline__ float of_key(int k) {
 }
 constexpr int kNoKey = static_cast<int>(0x807fffff);   // key_of(-inf)
 
+// e^x for x <= 0 (and -inf: 0): 2^(x log2 e), the rounding of the exponent made good.
+__device__ __forceinline__ float exp32(float x) {
+  x = fmaxf(x, -256.0f);
+  const float y = x * kLog2e;
+  const float more = fmaf(x, kLog2e, -y) + x * 1.92596299e-8f;
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fmaf(e, more * 0.693147181f, e);
+}
+
 __device__ __forceinline__ bool better(double v, int e, double bv, int be) {
   return v > bv || (v == bv && e < be);
 }
@@ -119,9 +128,6 @@ struct MaxI { __device__ __forceinline__ int operator()(int a, int b) const { re
 struct MinI { __device__ __forceinline__ int operator()(int a, int b) const { return a < b ? a : b; } };
 struct MaxF { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 struct Add { template <class T> __device__ __forceinline__ T operator()(T a, T b) const { return a + b; } };
-
-__device__ __forceinline__ float wave_max(float v) { return reduce<64>(v, MaxF()); }
-__device__ __forceinline__ double wave_sum(double v) { return reduce<64>(v, Add()); }
 
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-static_cast<double>(l))); }
 
@@ -361,15 +367,9 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
       sum = reduce<kL>(sum, Add());
       inv = sum > 0.0 ? 1.0 / sum : 0.0;
     } else if (!r.renorm) {
-      // exp(x) = 2^(x log2 e) with the product's rounding error made good
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float x = fmaxf(l[i] - top, -256.0f), y = x * kLog2e;
-        const float more = fmaf(x, kLog2e, -y) + x * 1.92596299e-8f;
-        const float ex = __builtin_amdgcn_exp2f(y);
-        sum += l[i] > kNegInf ? fmaf(ex, more * 0.693147181f, ex) : 0.0f;
-      }
+      for (int i = 0; i < V; ++i) sum += l[i] > kNegInf ? exp32(l[i] - top) : 0.0f;
       sum = reduce<kL>(sum, Add());
       inv = sum > 0.0f ? 1.0 / static_cast<double>(sum) : 0.0;
     }
@@ -599,95 +599,197 @@ void k_load_count(const int32_t* __restrict__ idx, int64_t n, int32_t E, int32_t
     if (hist[e]) __hip_atomic_fetch_add(load + e, hist[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <int VPL, bool BF16>
+// The backward.  Lane j of a token has its pick j; the token's row lies in LDS,
+// zero but for what the picks put there, and is written from there in whole
+// 16-byte pieces: the sparse gradients (V = 0) are the picks' own.  Dense
+// (softmax without renorm): with the picks' weights w in the row,
+//   D = sum_e s_e w_e,  dl_e = s_e (w_e - D),
+// the logits in registers, V of them to a lane, four neighbours at a time.
+// Bound by the row's write (and for the dense form its read).
+template <int kL, int V, bool BF16>
 __global__ __launch_bounds__(kWaves * kWave)
 void k_route_scored_bwd(RouterArgs r, const void* __restrict__ logits, int64_t ld, int32_t T,
                         const int32_t* __restrict__ idx, const float* __restrict__ dgate,
-                        void* __restrict__ dlogits, int64_t ldd) {
-  const int lane = lane_id();
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWaves + threadIdx.x / kWave;
-  if (t >= T) return;
-  const int E = r.E;
-  int e = lane < r.k ? idx[t * r.k + lane] : -1;
-  float l = kNegInf;
-  if (e >= 0 && e < E) l = clean_logit(load_logit<BF16>(logits, t * ld + e));
-  const bool valid = l > kNegInf;
-  if (!valid) e = -1;
-  const double x = static_cast<double>(l);
-  const double wg = valid ? static_cast<double>(r.scale) * static_cast<double>(dgate[t * r.k + lane]) : 0.0;
-  double s = 0.0, d = 0.0, rest = 0.0, top = 0.0;
-  double dense[VPL];                        // softmax without renorm: s of every expert
+                        void* __restrict__ dlogits, int64_t ldd, bool wide_in, bool wide_out) {
+  extern __shared__ float rows[];                       // [kWaves][tokens][E, a multiple of 4]
+  constexpr int kTok = kWave / kL;
+  const int lane = lane_id(), wave = threadIdx.x / kWave, sub = lane / kL, sl = lane & (kL - 1);
+  const int E = r.E, Ep = (E + 3) & ~3;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTok;
+  if (t0 >= T) return;
+  const int64_t t = t0 + sub < T ? t0 + sub : T - 1;
+  float* row = rows + (wave * kTok + sub) * Ep;
+  const auto fence = []() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); };
+
+  int e = sl < r.k ? idx[t * r.k + sl] : -1;
+  if (e < 0 || e >= E) e = -1;
+  float x = e >= 0 ? r.scale * dgate[t * r.k + sl] : 0.0f;
+  float lv[V > 0 ? V : 1];
+  if constexpr (V > 0) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) dense[i] = 0.0;
-  if (r.sigmoid && valid) s = 1.0 / (1.0 + exp(-x));
-  const double not_s = r.sigmoid ? (valid ? 1.0 / (1.0 + exp(x)) : 0.0) : 1.0;
-  if (r.renorm) {
-    const double u = share<64>(valid, l, r.sigmoid, s);
-    d = u * not_s * (wg - wave_sum(wg * u));
-  } else if (r.sigmoid) {
-    d = s * not_s * wg;
-  } else {
-    float lv[VPL], m = kNegInf;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int o = lane + kWave * i;
-      lv[i] = o < E ? clean_logit(load_logit<BF16>(logits, t * ld + o)) : kNegInf;
-      m = fmaxf(m, lv[i]);
+    for (int i = 0; i < V; i += 4) {
+      const int c = i * kL + 4 * sl;
+      float4 q = make_float4(kNegInf, kNegInf, kNegInf, kNegInf);
+      if (wide_in) {
+        if (c < E) {
+          if constexpr (BF16) {
+            const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(logits) + t * ld + c);
+            q = make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                            __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+          } else {
+            q = *reinterpret_cast<const float4*>(static_cast<const float*>(logits) + t * ld + c);
+          }
+        }
+      } else {
+        if (c < E) q.x = load_logit<BF16>(logits, t * ld + c);
+        if (c + 1 < E) q.y = load_logit<BF16>(logits, t * ld + c + 1);
+        if (c + 2 < E) q.z = load_logit<BF16>(logits, t * ld + c + 2);
+        if (c + 3 < E) q.w = load_logit<BF16>(logits, t * ld + c + 3);
+      }
+      lv[i] = clean_logit(q.x); lv[i + 1] = clean_logit(q.y);
+      lv[i + 2] = clean_logit(q.z); lv[i + 3] = clean_logit(q.w);
     }
-    top = static_cast<double>(wave_max(m));
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      dense[i] = lv[i] > kNegInf ? exp(static_cast<double>(lv[i]) - top) : 0.0;
-      sum += dense[i];
+  }
+  for (int c = 4 * sl; c < Ep; c += 4 * kL)
+    *reinterpret_cast<float4*>(row + c) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+
+  if constexpr (V == 0) {
+    const float l = e >= 0 ? clean_logit(load_logit<BF16>(logits, t * ld + e)) : kNegInf;
+    if (!(l > kNegInf)) {
+      e = -1;
+      x = 0.0f;
     }
-    sum = wave_sum(sum);
-    const double inv = sum > 0.0 ? 1.0 / sum : 0.0;
-    s = valid ? exp(x - top) * inv : 0.0;
-    d = s * wg;
-    rest = wave_sum(d);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) dense[i] *= -inv * rest;
+    const bool valid = e >= 0;
+    float s = 0.0f, not_s = 1.0f, big = 1.0f;
+    if (r.sigmoid) {
+      const float ex = exp32(-fabsf(l));                // of the smaller of s and 1 - s
+      big = 1.0f / (1.0f + ex);
+      const float small = ex * big;
+      s = l > 0.0f ? big : small;
+      not_s = l > 0.0f ? small : big;
+    }
+    if (r.renorm) {
+      const float lmax = of_key(reduce<kL>(valid ? key_of(l) : kNoKey, MaxI()));
+      // shares from exp(l - max); sigmoid: s = e^l / (1 + e^l), so that no s leaves the normal
+      // numbers while its share does not
+      float a = s;
+      if (!r.sigmoid || lmax <= 0.0f) a = exp32(l - lmax) * big;
+      a = valid ? a : 0.0f;
+      const float sum = reduce<kL>(a, Add());
+      const float u = valid ? a / sum : 0.0f;
+      x = u * not_s * (x - reduce<kL>(x * u, Add()));
+    } else {
+      x = s * not_s * x;
+    }
+    x = valid ? x : 0.0f;
   }
-  for (int j = 0; j < r.k; ++j) {
-    const int ej = __shfl(e, j);
-    const double dj = __shfl(d, j);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane + kWave * i == ej) dense[i] += dj;
+
+  // the picks into the row: each writes its lane and looks whether another was there
+  const bool valid = e >= 0;
+  fence();
+  if (valid) row[e] = __int_as_float(sl);
+  fence();
+  const bool twice = valid && __float_as_int(row[e]) != sl;
+  fence();
+  if (__ballot(twice) == 0) {
+    if (valid) row[e] = x;
+  } else {                                              // an id twice: added in the picks' order
+    if (valid) row[e] = 0.0f;
+    fence();
+    for (int j = 0; j < r.k; ++j) {
+      if (valid && sl == j) row[e] += x;
+      fence();
+    }
   }
+  fence();
+  __builtin_amdgcn_wave_barrier();
+
+  if constexpr (V > 0) {
+    float m = kNegInf;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int o = lane + kWave * i;
-    if (o >= E) continue;
-    if constexpr (BF16)
-      static_cast<uint16_t*>(dlogits)[t * ldd + o] = f32_to_bf16(static_cast<float>(dense[i]));
-    else
-      static_cast<float*>(dlogits)[t * ldd + o] = static_cast<float>(dense[i]);
+    for (int i = 0; i < V; ++i) m = fmaxf(m, lv[i]);
+    const float top = of_key(reduce<kL>(key_of(m), MaxI()));
+    float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const int c = i * kL + 4 * sl;
+      const float4 w = c < Ep ? *reinterpret_cast<const float4*>(row + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float wv[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = lv[i + j] > kNegInf ? exp32(lv[i + j] - top) : 0.0f;
+        sum += p;
+        dot += lv[i + j] > kNegInf ? p * wv[j] : 0.0f;
+        lv[i + j] = lv[i + j] > kNegInf ? p : -1.0f;    // not eligible: no gradient
+      }
+    }
+    sum = reduce<kL>(sum, Add());
+    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+    const float D = reduce<kL>(dot, Add()) * inv;
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const int c = i * kL + 4 * sl;
+      if (c >= Ep) continue;
+      const float4 w = *reinterpret_cast<const float4*>(row + c);
+      const float4 o = make_float4(lv[i] >= 0.0f ? lv[i] * inv * (w.x - D) : 0.0f,
+                                   lv[i + 1] >= 0.0f ? lv[i + 1] * inv * (w.y - D) : 0.0f,
+                                   lv[i + 2] >= 0.0f ? lv[i + 2] * inv * (w.z - D) : 0.0f,
+                                   lv[i + 3] >= 0.0f ? lv[i + 3] * inv * (w.w - D) : 0.0f);
+      *reinterpret_cast<float4*>(row + c) = o;
+    }
+    fence();
+    __builtin_amdgcn_wave_barrier();
+  }
+
+#pragma unroll
+  for (int u = 0; u < kTok; ++u) {
+    if (t0 + u >= T) break;
+    const float* from = rows + (wave * kTok + u) * Ep;
+    const int64_t to = (t0 + u) * ldd;
+    if (wide_out) {
+      for (int c = 4 * lane; c < E; c += 4 * kWave) {
+        const float4 q = *reinterpret_cast<const float4*>(from + c);
+        if constexpr (BF16)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dlogits) + to + c) =
+              make_uint2(pack_bf16x2(q.x, q.y), pack_bf16x2(q.z, q.w));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(dlogits) + to + c) = q;
+      }
+    } else {
+      for (int c = lane; c < E; c += kWave) {
+        if constexpr (BF16) static_cast<uint16_t*>(dlogits)[to + c] = f32_to_bf16(from[c]);
+        else static_cast<float*>(dlogits)[to + c] = from[c];
+      }
+    }
   }
 }
 
-constexpr int kBiasThreads = 256;
+// The bias update: one workgroup per layer, an expert to a thread as far as
+// 1024 threads go.  The load's sum in 64-bit integers, then the bias.  Launch
+// latency: 2 us for any size up to 1024 experts.
+constexpr int kBiasThreads = 1024;
 
-// One workgroup per layer: the load's sum in 64-bit integers, then the bias.
 __global__ __launch_bounds__(kBiasThreads)
 void k_bias_update(int32_t* __restrict__ load, int32_t E, float rate, float* __restrict__ bias,
                    int32_t clear_load) {
   __shared__ int64_t part[kBiasThreads / kWave];
   load += static_cast<int64_t>(blockIdx.x) * E;
   bias += static_cast<int64_t>(blockIdx.x) * E;
-  int64_t sum = 0;
-  for (int e = threadIdx.x; e < E; e += kBiasThreads) sum += load[e];
+  const int n = blockDim.x, first = threadIdx.x;
+  const int32_t mine = first < E ? load[first] : 0;
+  const float old = first < E ? bias[first] : 0.0f;
+  int64_t sum = mine;
+  for (int e = first + n; e < E; e += n) sum += load[e];
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o);
-  if (lane_id() == 0) part[threadIdx.x / kWave] = sum;
+  if (lane_id() == 0) part[first / kWave] = sum;
   __syncthreads();
   sum = 0;
-#pragma unroll
-  for (int w = 0; w < kBiasThreads / kWave; ++w) sum += part[w];
-  for (int e = threadIdx.x; e < E; e += kBiasThreads) {
-    const int64_t d = sum - static_cast<int64_t>(E) * load[e];
-    if (d != 0) bias[e] += d > 0 ? rate : -rate;
+  for (int w = 0; w < n / kWave; ++w) sum += part[w];
+  for (int e = first; e < E; e += n) {
+    const int64_t d = sum - static_cast<int64_t>(E) * (e == first ? mine : load[e]);
+    const float b = e == first ? old : bias[e];
+    bias[e] = b + (d > 0 ? rate : d < 0 ? -rate : 0.0f);
     if (clear_load) load[e] = 0;
   }
 }
@@ -728,17 +830,22 @@ bool split_row(RouterArgs& r, int kL, int max_chunk) {
   return r.chunk <= max_chunk;
 }
 
-template <int VPL>
-hipError_t launch_bwd_vpl(const RouterArgs& r, const void* logits, bool bf16, int64_t ld, int32_t T,
-                          const int32_t* idx, const float* dgate, void* dlogits, int64_t ldd,
-                          hipStream_t s) {
-  const dim3 grid((T + kWaves - 1) / kWaves), block(kWaves * kWave);
+template <int kL, int V>
+hipError_t launch_bwd_v(const RouterArgs& r, const void* logits, bool bf16, int64_t ld, int32_t T,
+                        const int32_t* idx, const float* dgate, void* dlogits, int64_t ldd,
+                        hipStream_t s) {
+  constexpr int kTok = kWaves * (kWave / kL);
+  const dim3 grid((T + kTok - 1) / kTok), block(kWaves * kWave);
+  const size_t lds = static_cast<size_t>(kTok) * ((r.E + 3) & ~3) * sizeof(float);
+  const uintptr_t bytes = bf16 ? 8 : 16;
+  const bool in = r.E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % bytes == 0;
+  const bool out = r.E % 4 == 0 && ldd % 4 == 0 && reinterpret_cast<uintptr_t>(dlogits) % bytes == 0;
   if (bf16)
-    hipLaunchKernelGGL((k_route_scored_bwd<VPL, true>), grid, block, 0, s, r, logits, ld, T, idx,
-                       dgate, dlogits, ldd);
+    hipLaunchKernelGGL((k_route_scored_bwd<kL, V, true>), grid, block, lds, s, r, logits, ld, T, idx,
+                       dgate, dlogits, ldd, in, out);
   else
-    hipLaunchKernelGGL((k_route_scored_bwd<VPL, false>), grid, block, 0, s, r, logits, ld, T, idx,
-                       dgate, dlogits, ldd);
+    hipLaunchKernelGGL((k_route_scored_bwd<kL, V, false>), grid, block, lds, s, r, logits, ld, T, idx,
+                       dgate, dlogits, ldd, in, out);
   return hipGetLastError();
 }
 
@@ -779,19 +886,27 @@ hipError_t launch_route_scored_bwd(const RouterArgs& r, const void* logits, bool
                                    void* dlogits, int64_t ldd, hipStream_t s) {
   if (T == 0) return hipSuccess;
   const int E = r.E;
-  if (E <= 64) return launch_bwd_vpl<1>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
-  if (E <= 128) return launch_bwd_vpl<2>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
-  if (E <= 256) return launch_bwd_vpl<4>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
-  if (E <= 512) return launch_bwd_vpl<8>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
-  if (E <= 1024) return launch_bwd_vpl<16>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
-  if (E <= 2048) return launch_bwd_vpl<32>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
-  return launch_bwd_vpl<64>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  const bool dense = !r.sigmoid && !r.renorm;
+  if (T >= kManyTokens && r.k <= 16 && E <= 512) {      // four tokens to a wave
+    if (!dense) return launch_bwd_v<16, 0>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+    if (E <= 64) return launch_bwd_v<16, 4>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+    if (E <= 128) return launch_bwd_v<16, 8>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+    if (E <= 256) return launch_bwd_v<16, 16>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+    return launch_bwd_v<16, 32>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  }
+  if (!dense) return launch_bwd_v<64, 0>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  if (E <= 256) return launch_bwd_v<64, 4>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  if (E <= 512) return launch_bwd_v<64, 8>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  if (E <= 1024) return launch_bwd_v<64, 16>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  if (E <= 2048) return launch_bwd_v<64, 32>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
+  return launch_bwd_v<64, 64>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
 }
 
 hipError_t launch_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate, float* bias,
                               bool clear_load, hipStream_t s) {
   if (n_layers == 0) return hipSuccess;
-  hipLaunchKernelGGL(k_bias_update, dim3(n_layers), dim3(kBiasThreads), 0, s, load, E, rate, bias,
+  const int threads = E < kBiasThreads ? (E + kWave - 1) / kWave * kWave : kBiasThreads;
+  hipLaunchKernelGGL(k_bias_update, dim3(n_layers), dim3(threads), 0, s, load, E, rate, bias,
                      clear_load ? 1 : 0);
   return hipGetLastError();
 }
