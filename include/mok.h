@@ -668,15 +668,29 @@ typedef struct {
     int32_t skip;        /* not 0: nothing is written (a step with overflow)     */
 } mok_adamw_scalars;
 
-/* One step over n_tensors tensors (tensors, hyper: host, read before the call
- * returns).  scalars: NULL, or device memory (16-byte aligned) whose four
- * numbers are used in place of hyper's lr, grad_scale and step.  Updates p, m
- * and v in place.  One launch for up to 44 tensors with n > 0.  No two buffers
- * that the step writes may overlap; overlapping p are refused
- * (MOK_ERR_INVALID_ARG).  fp32 pointers must be 4-byte, bf16 pointers 2-byte
- * aligned; tensors whose pointers are all aligned for 4 elements (16 bytes of
- * fp32) go faster. */
-mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t n_tensors,
+/* The list of tensors of a program's steps: their addresses and factors in a
+ * table in device memory (16-byte aligned, mok_adamw_table_size(n_tensors)
+ * bytes, the caller's), written by mok_adamw_build_table in stream order from
+ * the host list (read before the call returns), and a plan of its units, which
+ * the host keeps (private to the library).  Table and plan serve any number of
+ * steps, on any stream that comes after the writing, as long as the tensors
+ * stay where they are.  No two buffers that a step writes may overlap;
+ * overlapping p are refused (MOK_ERR_INVALID_ARG).  fp32 pointers must be
+ * 4-byte, bf16 pointers 2-byte aligned; tensors whose pointers are all aligned
+ * for 4 elements (16 bytes of fp32) go faster. */
+typedef struct {
+    int64_t n_units[2];        /* of fp32 states, of 8-bit states */
+    int32_t n_tensors[2], list, reserved;
+} mok_adamw_plan;
+
+size_t mok_adamw_table_size(int32_t n_tensors);
+mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tensors, void* table,
+                                 size_t table_bytes, mok_adamw_plan* plan, hipStream_t stream);
+
+/* One step over a list (hyper: host).  scalars: NULL, or device memory (16-byte
+ * aligned) whose four numbers are used in place of hyper's lr, grad_scale and
+ * step.  Updates p, m and v in place, in one launch for each state format. */
+mok_status mok_adamw_step(const void* table, const mok_adamw_plan* plan,
                           const mok_adamw_hyper* hyper, const mok_adamw_scalars* scalars,
                           hipStream_t stream);
 

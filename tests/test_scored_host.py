@@ -89,11 +89,9 @@ def _tensor(**kw):
     return mok.mok_adamw_tensor(**d)
 
 
-def _step(tensors, scalars=None, **kw):
-    h = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, grad_scale=1.0, step=1)
-    h.update(kw)
+def _build(tensors, table=64, size=1 << 20):
     a = (mok.mok_adamw_tensor * max(len(tensors), 1))(*tensors)
-    return L.mok_adamw_step(a, len(tensors), C.byref(mok.mok_adamw_hyper(**h)), scalars, None)
+    return L.mok_adamw_build_table(a, len(tensors), table, size, C.byref(mok.mok_adamw_plan()), None)
 
 
 @pytest.mark.parametrize("bad", [dict(n=-1), dict(grad_type=2), dict(state_format=2), dict(p=None), dict(grad=None),
@@ -101,25 +99,50 @@ def _step(tensors, scalars=None, **kw):
                                  dict(p=(1 << 20) + 2), dict(p_bf16=65), dict(grad=66), dict(grad=65, grad_type=1),
                                  dict(m=66), dict(v=66), dict(lr_scale=float("nan")), dict(weight_decay=float("inf"))])
 def test_bad_adamw_tensor_refused(bad):
-    assert _step([_tensor(**bad)]) == E_ARG
-    assert _step([_tensor(p=9 << 20), _tensor(**bad)]) == E_ARG
+    assert _build([_tensor(**bad)]) == E_ARG
+    assert _build([_tensor(p=9 << 20), _tensor(**bad)]) == E_ARG
 
 
-def test_adamw_refusals():
+def test_adamw_table_refusals():
     t = _tensor()
+    assert _build([t, t]) == E_ARG                                         # the same tensor twice
+    assert _build([t, _tensor(p=(1 << 20) + 64 * 4 - 4)]) == E_ARG         # overlapping parameters
+    assert _build([_tensor(n=1 << 62)]) == E_UNS
+    far = [_tensor(p=i << 50, n=1 << 40) for i in range(1, 4)]             # more units than a launch has
+    assert _build(far) == E_UNS
+    assert _build([t], table=None) == E_ARG
+    assert _build([t], table=72) == E_ARG                                  # not 16-byte aligned
+    need = mok.mok_adamw_table_size(1)
+    assert need > 0 and mok.mok_adamw_table_size(3) > need and mok.mok_adamw_table_size(-1) == 0
+    assert _build([t], size=need - 1) == E_WS
+    a, plan = (mok.mok_adamw_tensor * 1)(t), mok.mok_adamw_plan()
+    assert L.mok_adamw_build_table(None, 1, 64, 1 << 20, C.byref(plan), None) == E_ARG
+    assert L.mok_adamw_build_table(a, -1, 64, 1 << 20, C.byref(plan), None) == E_ARG
+    assert L.mok_adamw_build_table(a, 1, 64, 1 << 20, None, None) == E_ARG
+    assert _build([]) == mok.MOK_OK
+    assert _build([_tensor(n=0, p=None)]) == mok.MOK_OK                    # nothing to do
+
+
+def test_adamw_step_refusals():
+    def step(plan=dict(n_units=(1, 0), n_tensors=(1, 0), list=1), table=64, scalars=None, **kw):
+        h = dict(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, grad_scale=1.0, step=1)
+        h.update(kw)
+        p = mok.mok_adamw_plan((C.c_int64 * 2)(*plan.get("n_units", (0, 0))),
+                               (C.c_int32 * 2)(*plan.get("n_tensors", (0, 0))), plan.get("list", 0))
+        return L.mok_adamw_step(table, C.byref(p), C.byref(mok.mok_adamw_hyper(**h)),
+                                scalars, None)
     for bad in (dict(lr=float("nan")), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=float("nan")),
                 dict(eps=-1.0), dict(eps=float("inf")), dict(grad_scale=float("inf")), dict(step=0), dict(step=-3)):
-        assert _step([t], **bad) == E_ARG, bad
-    assert _step([t], scalars=8) == E_ARG                                  # not 16-byte aligned
-    assert _step([t, t]) == E_ARG                                          # the same tensor twice
-    assert _step([t, _tensor(p=(1 << 20) + 64 * 4 - 4)]) == E_ARG          # overlapping parameters
-    assert _step([_tensor(n=1 << 62)]) == E_UNS
-    assert L.mok_adamw_step(None, 1, C.byref(mok.mok_adamw_hyper(step=1)), None, None) == E_ARG
-    assert L.mok_adamw_step(None, -1, C.byref(mok.mok_adamw_hyper(step=1)), None, None) == E_ARG
-    a = (mok.mok_adamw_tensor * 1)(t)
-    assert L.mok_adamw_step(a, 1, None, None, None) == E_ARG
-    assert _step([]) == mok.MOK_OK
-    assert _step([_tensor(n=0, p=None)]) == mok.MOK_OK                     # nothing to do
+        assert step(**bad) == E_ARG, bad
+    assert step(scalars=8) == E_ARG                                        # not 16-byte aligned
+    assert step(table=None) == E_ARG
+    for plan in (dict(n_units=(-1, 0)), dict(n_units=(1, 0)), dict(n_units=(0, 1), n_tensors=(1, 0), list=1),
+                 dict(n_units=(0, 1 << 31), n_tensors=(0, 1), list=1), dict(n_units=(1, 0), n_tensors=(-1, 0)),
+                 dict(n_units=(1, 0), n_tensors=(2, 0), list=1), dict(n_units=(1, 1), n_tensors=(1, 1), list=1)):
+        assert step(plan=plan) == E_ARG, plan
+    assert step(plan={}, table=None) == mok.MOK_OK                         # an empty list
+    assert L.mok_adamw_step(64, None, C.byref(mok.mok_adamw_hyper(step=1)), None, None) == E_ARG
+    assert L.mok_adamw_step(64, C.byref(mok.mok_adamw_plan()), None, None, None) == E_ARG
 
 
 def test_binding_refuses_wrong_tensors():

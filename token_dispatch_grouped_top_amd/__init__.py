@@ -74,6 +74,11 @@ class mok_adamw_hyper(C.Structure):
         ("step", C.c_int32), ("seed", C.c_uint32)]
 
 
+class mok_adamw_plan(C.Structure):
+    _fields_ = [("n_units", C.c_int64 * 2), ("n_tensors", C.c_int32 * 2), ("list", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
 _P, _I32, _I64, _SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 _DESC, _TOK = C.POINTER(mok_layer_desc), C.POINTER(mok_tokens)
 _RTR = C.POINTER(mok_router_desc)
@@ -82,8 +87,10 @@ _SIGS = {
     "mok_route_scored": (C.c_int, [_RTR, _P, _I32, _I64, _P, _I32, _P, _P, _P, _P]),
     "mok_route_scored_backward": (C.c_int, [_RTR, _P, _I32, _I64, _I32, _P, _P, _P, _I64, _P]),
     "mok_route_bias_update": (C.c_int, [_P, _I32, _I32, C.c_float, _P, _I32, _P]),
-    "mok_adamw_step": (C.c_int, [C.POINTER(mok_adamw_tensor), _I32, C.POINTER(mok_adamw_hyper),
-                                 _P, _P]),
+    "mok_adamw_table_size": (_SZ, [_I32]),
+    "mok_adamw_build_table": (C.c_int, [C.POINTER(mok_adamw_tensor), _I32, _P, _SZ,
+                                        C.POINTER(mok_adamw_plan), _P]),
+    "mok_adamw_step": (C.c_int, [_P, C.POINTER(mok_adamw_plan), C.POINTER(mok_adamw_hyper), _P, _P]),
     "mok_moe_forward_scored": (C.c_int, [_DESC, _RTR, _P, _I32, _I64, _P, _I32, _P, _P, _P, _TOK,
                                          _P, _P, _TOK, _P, _SZ, _P]),
     "mok_route_gemm_workspace_size": (_SZ, [_I32, _I32, _I32]),
@@ -287,15 +294,17 @@ def mok_route_bias_update(load, n_layers: int, E: int, rate: float, bias, clear_
 
 
 class AdamwTensors:
-    """Tensors of an AdamW step (a host array of ``mok_adamw_tensor`` plus what keeps them alive).
+    """Tensors of an AdamW step: the device table of ``mok_adamw_build_table``, its plan, and what
+    keeps the tensors alive.
 
     One dict per tensor: ``p`` (fp32), ``grad`` (fp32 or bf16), ``m`` and ``v`` (fp32, or uint8
     codes beside ``m_scale`` and ``v_scale``, uint8), and optionally ``p_bf16``, ``lr_scale`` (1)
     and ``weight_decay`` (0).  Dense tensors of the same number of elements on one GPU.  Built
-    once for a program's buffers.
+    once for a program's buffers, on the stream given (waited for, unless it is being captured:
+    the list can then be used on any stream).
     """
 
-    def __init__(self, tensors: Sequence[dict]):
+    def __init__(self, tensors: Sequence[dict], stream=None):
         self.tensors = [dict(t) for t in tensors]
         self.c = (mok_adamw_tensor * len(self.tensors))()
         f32, u8 = (torch.float32,), (torch.uint8,)
@@ -318,6 +327,23 @@ class AdamwTensors:
             c.n, c.grad_type = n, _TYPES[t["grad"].dtype]
             c.state_format = MOK_STATE_MXFP8 if coded else MOK_STATE_F32
             c.lr_scale, c.weight_decay = t.get("lr_scale", 1.0), t.get("weight_decay", 0.0)
+        self.plan, self.table = mok_adamw_plan(), None
+        if self.tensors:
+            size = mok_adamw_table_size(len(self.c))
+            self.table = torch.empty(size, dtype=torch.uint8, device=self.tensors[0]["p"].device)
+            mok_adamw_build_table(self.c, self.table, self.plan, stream)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.synchronize()
+
+
+def mok_adamw_table_size(n_tensors: int) -> int:
+    return int(_lib.mok_adamw_table_size(n_tensors))
+
+
+def mok_adamw_build_table(tensors, table, plan: mok_adamw_plan, stream=None) -> None:
+    """tensors: a ctypes array of mok_adamw_tensor; table: dense bytes on the GPU; plan: filled in."""
+    _check(_lib.mok_adamw_build_table(tensors, len(tensors), _ptr(table), _ws_bytes(table, None),
+                                      C.byref(plan), _stream(stream)), "mok_adamw_build_table")
 
 
 def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float, eps: float,
@@ -330,7 +356,7 @@ def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float,
             raise ValueError("scalars: 16 dense bytes are wanted")
         scalars = _on_device(scalars, "scalars")
     h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
-    _check(_lib.mok_adamw_step(tensors.c, len(tensors.c), C.byref(h), scalars or 0,
+    _check(_lib.mok_adamw_step(_ptr(tensors.table), C.byref(tensors.plan), C.byref(h), scalars or 0,
                                _stream(stream)), "mok_adamw_step")
 
 

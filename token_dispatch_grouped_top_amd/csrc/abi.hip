@@ -263,16 +263,15 @@ mok_status mok_route_bias_update(int32_t* load, int32_t n_layers, int32_t E, flo
   return hip_status(launch_bias_update(load, n_layers, E, rate, bias, clear_load != 0, stream));
 }
 
-mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t n_tensors,
-                          const mok_adamw_hyper* hyper, const mok_adamw_scalars* scalars,
-                          hipStream_t stream) {
-  if (n_tensors < 0 || !hyper || (n_tensors > 0 && !tensors)) return MOK_ERR_INVALID_ARG;
-  const mok_adamw_hyper& h = *hyper;
-  if (!std::isfinite(h.lr) || !std::isfinite(h.eps) || h.eps < 0.0 || !std::isfinite(h.grad_scale) ||
-      !(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0))
-    return MOK_ERR_INVALID_ARG;
-  if (!scalars && h.step < 1) return MOK_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(scalars) % 16 != 0) return MOK_ERR_INVALID_ARG;
+size_t mok_adamw_table_size(int32_t n_tensors) {
+  return n_tensors < 0 ? 0 : adamw_table_bytes(n_tensors);
+}
+
+mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tensors, void* table,
+                                 size_t table_bytes, mok_adamw_plan* plan, hipStream_t stream) {
+  if (n_tensors < 0 || !plan || (n_tensors > 0 && (!tensors || !table))) return MOK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(table) % 16 != 0) return MOK_ERR_INVALID_ARG;
+  int64_t units = 0;
   try {
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // [begin, end) of every p
     spans.reserve(n_tensors);
@@ -285,6 +284,7 @@ mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t n_tensors,
         return MOK_ERR_INVALID_ARG;
       if (x.n == 0) continue;
       if (x.n > adamw_max_elements()) return MOK_ERR_UNSUPPORTED;
+      units += x.n / 1024 + 1;
       const bool mx = x.state_format == MOK_STATE_MXFP8;
       if (!x.p || !x.grad || !x.m || !x.v || (mx && (!x.m_scale || !x.v_scale)))
         return MOK_ERR_INVALID_ARG;
@@ -301,7 +301,29 @@ mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t n_tensors,
   } catch (const std::bad_alloc&) {
     return MOK_ERR_UNSUPPORTED;
   }
-  return hip_status(launch_adamw(tensors, n_tensors, h, scalars, stream));
+  if (units > 0x7fffffff) return MOK_ERR_UNSUPPORTED;      // one launch's grid
+  if (n_tensors > 0 && table_bytes < adamw_table_bytes(n_tensors)) return MOK_ERR_WORKSPACE;
+  *plan = mok_adamw_plan{};
+  return hip_status(launch_adamw_table(tensors, n_tensors, table, *plan, stream));
+}
+
+mok_status mok_adamw_step(const void* table, const mok_adamw_plan* plan,
+                          const mok_adamw_hyper* hyper, const mok_adamw_scalars* scalars,
+                          hipStream_t stream) {
+  if (!plan || !hyper) return MOK_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)
+    if (plan->n_units[i] < 0 || plan->n_units[i] > 0x7fffffff || plan->n_tensors[i] < 0 ||
+        (plan->n_units[i] > 0 && (plan->n_tensors[i] < 1 || !table)))
+      return MOK_ERR_INVALID_ARG;
+  if (plan->list < static_cast<int64_t>(plan->n_tensors[0]) + plan->n_tensors[1])
+    return MOK_ERR_INVALID_ARG;
+  const mok_adamw_hyper& h = *hyper;
+  if (!std::isfinite(h.lr) || !std::isfinite(h.eps) || h.eps < 0.0 || !std::isfinite(h.grad_scale) ||
+      !(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0))
+    return MOK_ERR_INVALID_ARG;
+  if (!scalars && h.step < 1) return MOK_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(scalars) % 16 != 0) return MOK_ERR_INVALID_ARG;
+  return hip_status(launch_adamw(table, *plan, h, scalars, stream));
 }
 
 size_t mok_route_gemm_workspace_size(int32_t T, int32_t E, int32_t H) {

@@ -1,15 +1,22 @@
-// adamw.hip -- one AdamW step over many tensors in one launch, states in fp32
-// or in E4M3 codes with a scale per 32 elements.
+// adamw.hip -- one AdamW step over many tensors, states in fp32 or in E4M3 codes
+// with a scale per 32 elements: one launch for each of the two.
 //
-// The tensors' pointers travel as a kernel argument (up to kMaxTensors per
-// launch), so the call needs no device table.  A workgroup takes one unit of
-// kUnit elements of one tensor: the unit's tensor is the last whose first unit
-// is not behind it, found with one load per lane and a ballot.  A thread works
-// on four consecutive elements at a time, so that every access of a wave is
-// contiguous, and the 32 elements of an 8-bit block lie in eight lanes.
+// A table in device memory, written once for a program's buffers, holds the
+// tensors' addresses and factors, and the first unit of each: the 1024 elements
+// (2048 with 8-bit states) of one workgroup.  Small units keep what is in flight
+// at any time in one run of memory: 352 M elements with fp32 states take 1.62 ms
+// so, 1.85 ms in units of 8192, and 2.0 ms where 2048 workgroups take the units
+// in turn and drift apart.  A workgroup finds its tensor with one load per lane
+// and a ballot for each power of 64 in the number of tensors, and works out the
+// step's factors while its elements are on their way.  A thread has four
+// consecutive elements, so that every access of a wave is contiguous and the 32
+// elements of an 8-bit block lie in eight lanes.
 //
-// The order of the fp32 operations is fixed (no contraction): the 8-bit codes
-// follow from the bits of m and v.
+// Bound by HBM: 28 bytes an element with fp32 states, bf16 gradients and copy,
+// 16 1/8 with 8-bit states.
+//
+// The order of the fp32 operations on the states is fixed (no contraction): the
+// 8-bit codes follow from the bits of m and v.
 #include "mok_internal.h"
 
 namespace mok {
@@ -17,9 +24,10 @@ namespace mok {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSteps = 4;                         // groups of four per thread and unit
-constexpr int kUnit = kThreads * 4 * kSteps;      // elements
-constexpr int kMaxTensors = kAdamwMaxTensors;
+constexpr int kGroup = kThreads * 4;              // elements of a workgroup at a time
+constexpr int kBatch = 40;                        // tensors of one table-writing launch
+constexpr int kF32Waves = 5, kMxWaves = 7;
+constexpr int kMxGroups = 2;                      // groups of a unit with 8-bit states
 
 struct TensorArg {
   float* p;
@@ -30,11 +38,28 @@ struct TensorArg {
   uint8_t* ms;
   uint8_t* vs;
   int64_t n;
-  uint32_t flags;                                 // kBf16Grad, kMx, kWide
-  uint32_t number;                                // of the tensor in the call
+  uint32_t flags;                                 // kBf16Grad, kWide
+  uint32_t number;                                // of the tensor in the caller's list
   float lr_scale, weight_decay;
+  int64_t unit0;
 };
-constexpr uint32_t kBf16Grad = 1, kMx = 2, kWide = 4;
+constexpr uint32_t kBf16Grad = 1, kWide = 2;
+
+struct TableArg {
+  int32_t first, count;
+  TensorArg t[kBatch];
+};
+static_assert(sizeof(TableArg) <= 4096, "kernel argument");
+
+// The table: n first units, then n descriptors.
+size_t descriptors_at(int64_t n) { return (static_cast<size_t>(n) * 8 + 15) / 16 * 16; }
+
+__global__ void k_adamw_table(TableArg a, int64_t* units, TensorArg* t) {
+  const int i = threadIdx.x;
+  if (i >= a.count) return;
+  units[a.first + i] = a.t[i].unit0;
+  t[a.first + i] = a.t[i];
+}
 
 struct StepArg {
   double lr, beta1, beta2;
@@ -42,15 +67,10 @@ struct StepArg {
   int32_t step;
   uint32_t seed;
   const mok_adamw_scalars* scalars;
+  const int64_t* units;
+  const TensorArg* tensors;
   int32_t n_tensors;
 };
-
-struct Args {
-  StepArg h;
-  uint32_t unit0[kMaxTensors];                    // first unit of each tensor
-  TensorArg t[kMaxTensors];
-};
-static_assert(sizeof(Args) <= 4096, "kernel argument");
 
 __device__ __forceinline__ uint32_t hash32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x9E3779B1u;
@@ -83,11 +103,13 @@ __device__ __forceinline__ bool finite(float x) {
   return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
 }
 
+// (b + 0.5) / 65536, exact.
 __device__ __forceinline__ float unit_of(uint32_t b16) {
-#pragma clang fp contract(off)
-  return (static_cast<float>(b16) + 0.5f) * (1.0f / 65536.0f);
+  return fmaf(static_cast<float>(b16), 1.0f / 65536.0f, 0.5f / 65536.0f);
 }
 
+// Codes of any value, and of those that most are: finite, a in [2^-6, 448]
+// (an E4M3 number without a subnormal, so its neighbours are cut from its bits).
 __device__ __forceinline__ uint32_t encode_m(float m, int E, uint32_t b16) {
 #pragma clang fp contract(off)
   if (!finite(m)) return 0x7fu;
@@ -96,6 +118,10 @@ __device__ __forceinline__ uint32_t encode_m(float m, int E, uint32_t b16) {
   const uint32_t tiny = static_cast<uint32_t>(a * 512.0f + unit_of(b16));
   const uint32_t code = a >= 0.015625f ? normal : tiny;
   return m < 0.0f ? code | 0x80u : code;
+}
+__device__ __forceinline__ uint32_t encode_m_normal(float a, float m, uint32_t b16) {
+  const uint32_t code = (__float_as_uint(a) + 16u * b16 + (8u - (960u << 20))) >> 20;
+  return code | ((__float_as_uint(m) >> 24) & 0x80u);
 }
 
 __device__ __forceinline__ uint32_t encode_r(float r, int E, uint32_t b16) {
@@ -110,125 +136,211 @@ __device__ __forceinline__ uint32_t encode_r(float r, int E, uint32_t b16) {
   code += have > unit_of(b16) * span ? 1u : 0u;
   return r > 0.0f && code == 0u ? 1u : code;
 }
+__device__ __forceinline__ uint32_t encode_r_normal(float a, uint32_t b16) {
+#pragma clang fp contract(off)
+  const uint32_t u = __float_as_uint(a) & 0xfff00000u;
+  const float low = __uint_as_float(u), high = __uint_as_float(u + 0x100000u);
+  const float have = (a - low) * (a + low), span = (high - low) * (high + low);
+  return (u >> 20) - 960u + (have > unit_of(b16) * span ? 1u : 0u);
+}
 
 struct Factors {
   float b1, c1, b2, c2, gs, keep, rate, inv_bc2, eps;
 };
 
-// One element: m, v (or r^2) and p updated; r = sqrt(v).
-__device__ __forceinline__ void update(const Factors& f, float g, float& p, float& m, float& v,
-                                       float& r) {
+// New m and v of one element.
+__device__ __forceinline__ void states(const Factors& f, float g, float& m, float& v) {
 #pragma clang fp contract(off)
   g = g * f.gs;
   m = f.b1 * m + f.c1 * g;
   v = f.b2 * v + f.c2 * g * g;
-  r = sqrtf(v);
-  p = p * f.keep - f.rate * (m / (r * f.inv_bc2 + f.eps));
+}
+
+// sqrt of a normal number: rsq and one step (rounds as sqrtf but for an odd case in 2^20).
+__device__ __forceinline__ float sqrt_normal(float v) {
+  const float y = __builtin_amdgcn_rsqf(v), s = v * y;
+  return fmaf(fmaf(-s, s, v), 0.5f * y, s);
+}
+
+__device__ __forceinline__ float parameter(const Factors& f, float p, float m, float r) {
+  const float d = fmaf(r, f.inv_bc2, f.eps);
+  return fmaf(-f.rate, m * __builtin_amdgcn_rcpf(d), p * f.keep);
 }
 
 // Largest of the eight lanes that share a block of 32 elements.
 __device__ __forceinline__ float max8(float v) {
-  v = fmaxf(v, __shfl_xor(v, 1));
-  v = fmaxf(v, __shfl_xor(v, 2));
-  return fmaxf(v, __shfl_xor(v, 4));
+  int b = __builtin_bit_cast(int, v);                    // not negative: ordered as integers
+  auto up = [&](int o) { b = o > b ? o : b; };
+  up(__builtin_amdgcn_update_dpp(0, b, 0xB1, 0xF, 0xF, true));
+  up(__builtin_amdgcn_update_dpp(0, b, 0x4E, 0xF, 0xF, true));
+  up(__builtin_amdgcn_update_dpp(0, b, 0x141, 0xF, 0xF, true));
+  return __builtin_bit_cast(float, b);
 }
 
-// Four elements from i0 on, of which `have` exist (0..4).  WIDE: 4, and every
-// pointer is aligned for them.
-template <bool MX, bool WIDE>
-__device__ __forceinline__ void group4(const TensorArg& t, const Factors& f, uint32_t key,
-                                       int64_t i0, int have) {
-  float p[4] = {}, g[4] = {}, m[4] = {}, v[4] = {}, r[4] = {};
-  const bool bf16 = t.flags & kBf16Grad;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Four elements as they are loaded.
+template <bool MX>
+struct Group {
+  f32x4 p;
+  f32x4 g;                       // bf16: two words
+  f32x4 m, v;                    // MX: one word of codes
+  int em, ev;                    // MX: old scales
+};
+
+// `have` of the four exist (0..4); whole: all, aligned.
+template <bool MX>
+__device__ __forceinline__ void load(const TensorArg& t, int64_t i0, int have, bool wide, Group<MX>& o) {
   const uint16_t* gb = static_cast<const uint16_t*>(t.g);
   const float* gf = static_cast<const float*>(t.g);
-  uint8_t* mc = static_cast<uint8_t*>(t.m);
-  uint8_t* vc = static_cast<uint8_t*>(t.v);
-  float* mf = static_cast<float*>(t.m);
-  float* vf = static_cast<float*>(t.v);
-  uint32_t mw = 0, vw = 0;
-  if (WIDE) {
-    const float4 a = *reinterpret_cast<const float4*>(t.p + i0);
-    p[0] = a.x; p[1] = a.y; p[2] = a.z; p[3] = a.w;
+  const uint8_t* mc = static_cast<const uint8_t*>(t.m);
+  const uint8_t* vc = static_cast<const uint8_t*>(t.v);
+  const float* mf = static_cast<const float*>(t.m);
+  const float* vf = static_cast<const float*>(t.v);
+  const bool bf16 = t.flags & kBf16Grad;
+  o.p = o.g = o.m = o.v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  o.em = o.ev = 0;
+  if (wide && have == 4) {
+    o.p = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(t.p + i0));
     if (bf16) {
-      const uint2 b = *reinterpret_cast<const uint2*>(gb + i0);
-      g[0] = __uint_as_float(b.x << 16); g[1] = __uint_as_float(b.x & 0xffff0000u);
-      g[2] = __uint_as_float(b.y << 16); g[3] = __uint_as_float(b.y & 0xffff0000u);
+      const u32x2 b = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(gb + i0));
+      o.g.x = __uint_as_float(b.x << 16); o.g.y = __uint_as_float(b.x & 0xffff0000u);
+      o.g.z = __uint_as_float(b.y << 16); o.g.w = __uint_as_float(b.y & 0xffff0000u);
     } else {
-      const float4 b = *reinterpret_cast<const float4*>(gf + i0);
-      g[0] = b.x; g[1] = b.y; g[2] = b.z; g[3] = b.w;
+      o.g = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(gf + i0));
     }
     if (MX) {
-      mw = *reinterpret_cast<const uint32_t*>(mc + i0);
-      vw = *reinterpret_cast<const uint32_t*>(vc + i0);
+      o.m.x = __uint_as_float(__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(mc + i0)));
+      o.v.x = __uint_as_float(__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(vc + i0)));
     } else {
-      const float4 b = *reinterpret_cast<const float4*>(mf + i0);
-      const float4 c = *reinterpret_cast<const float4*>(vf + i0);
-      m[0] = b.x; m[1] = b.y; m[2] = b.z; m[3] = b.w;
-      v[0] = c.x; v[1] = c.y; v[2] = c.z; v[3] = c.w;
+      o.m = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(mf + i0));
+      o.v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(vf + i0));
     }
   } else {
+    uint32_t mw = 0, vw = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j >= have) break;
-      p[j] = t.p[i0 + j];
-      g[j] = bf16 ? __uint_as_float(static_cast<uint32_t>(gb[i0 + j]) << 16) : gf[i0 + j];
+      o.p[j] = t.p[i0 + j];
+      o.g[j] = bf16 ? __uint_as_float(static_cast<uint32_t>(gb[i0 + j]) << 16) : gf[i0 + j];
       if (MX) {
         mw |= static_cast<uint32_t>(mc[i0 + j]) << (8 * j);
         vw |= static_cast<uint32_t>(vc[i0 + j]) << (8 * j);
       } else {
-        m[j] = mf[i0 + j];
-        v[j] = vf[i0 + j];
+        o.m[j] = mf[i0 + j];
+        o.v[j] = vf[i0 + j];
       }
+    }
+    if (MX) {
+      o.m.x = __uint_as_float(mw);
+      o.v.x = __uint_as_float(vw);
     }
   }
   if (MX && have > 0) {
-    const int em = t.ms[i0 >> 5] - 127, ev = t.vs[i0 >> 5] - 127;
+    o.em = t.ms[i0 >> 5];
+    o.ev = t.vs[i0 >> 5];
+  }
+}
+
+template <bool MX>
+__device__ __forceinline__ void work(const TensorArg& t, const Factors& f, uint32_t key, int64_t i0,
+                                     int have, bool wide, Group<MX>& o) {
+  float m[4], v[4], r[4], p[4];
+  uint32_t mw = __float_as_uint(o.m.x), vw = __float_as_uint(o.v.x);
+  if (MX) {
+#pragma clang fp contract(off)
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 m01 = __builtin_amdgcn_cvt_pk_f32_fp8(mw, false), m23 = __builtin_amdgcn_cvt_pk_f32_fp8(mw, true);
+    const f32x2 v01 = __builtin_amdgcn_cvt_pk_f32_fp8(vw, false), v23 = __builtin_amdgcn_cvt_pk_f32_fp8(vw, true);
+    m[0] = m01.x; m[1] = m01.y; m[2] = m23.x; m[3] = m23.y;
+    v[0] = v01.x; v[1] = v01.y; v[2] = v23.x; v[3] = v23.y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      m[j] = __builtin_amdgcn_ldexpf(e4m3_value((mw >> (8 * j)) & 0xffu), em);
-      const float q = __builtin_amdgcn_ldexpf(e4m3_value((vw >> (8 * j)) & 0xffu), ev);
+      m[j] = __builtin_amdgcn_ldexpf(m[j], o.em - 127);
+      const float q = __builtin_amdgcn_ldexpf(v[j], o.ev - 127);
       v[j] = q * q;
     }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { m[j] = o.m[j]; v[j] = o.v[j]; }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (WIDE || j < have) update(f, g[j], p[j], m[j], v[j], r[j]);
+  for (int j = 0; j < 4; ++j) {
+    states(f, o.g[j], m[j], v[j]);
+    if (MX && j >= have) m[j] = v[j] = 0.0f;
+  }
+  // the plain way for a wave with a value that is not finite, or v below the range of rsq
+  const float lowest = fminf(fminf(v[0], v[1]), fminf(v[2], v[3]));
+  const float all = (fabsf(m[0]) + fabsf(m[1])) + (fabsf(m[2]) + fabsf(m[3])) +
+                    ((v[0] + v[1]) + (v[2] + v[3]));
+  const bool odd = __ballot(!(lowest >= 0x1p-100f && all < __builtin_inff())) != 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = odd ? sqrtf(v[j]) : sqrt_normal(v[j]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = parameter(f, o.p[j], m[j], r[j]);
   if (MX) {
     float am = 0.0f, ar = 0.0f;
+    if (odd) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (WIDE || j < have) {
+      for (int j = 0; j < 4; ++j) {
         if (finite(m[j])) am = fmaxf(am, fabsf(m[j]));
         if (finite(r[j])) ar = fmaxf(ar, r[j]);
       }
+    } else {
+      am = fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3])));
+      ar = fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
+    }
     const int em = state_scale_exp(max8(am)), er = state_scale_exp(max8(ar));
-    mw = vw = 0;
+    uint32_t h[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint64_t i = static_cast<uint64_t>(i0) + j;
-      const uint32_t h = hash32(static_cast<uint32_t>(i) +
-                                static_cast<uint32_t>(i >> 32) * 0x6A09E667u + key);
-      mw |= encode_m(m[j], em, h & 0xffffu) << (8 * j);
-      vw |= encode_r(r[j], er, h >> 16) << (8 * j);
+      h[j] = hash32(static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x6A09E667u + key);
+    }
+    float a[4], b[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = __builtin_amdgcn_ldexpf(fabsf(m[j]), -em);
+      b[j] = __builtin_amdgcn_ldexpf(r[j], -er);
+    }
+    const float least = fminf(fminf(fminf(a[0], a[1]), fminf(a[2], a[3])),
+                              fminf(fminf(b[0], b[1]), fminf(b[2], b[3])));
+    mw = vw = 0;
+    if (odd || __ballot(!(least >= 0.015625f))) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mw |= encode_m(m[j], em, h[j] & 0xffffu) << (8 * j);
+        vw |= encode_r(r[j], er, h[j] >> 16) << (8 * j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mw |= encode_m_normal(a[j], m[j], h[j] & 0xffffu) << (8 * j);
+        vw |= encode_r_normal(b[j], h[j] >> 16) << (8 * j);
+      }
     }
     if (have > 0 && (i0 & 31) == 0) {
       t.ms[i0 >> 5] = static_cast<uint8_t>(em + 127);
       t.vs[i0 >> 5] = static_cast<uint8_t>(er + 127);
     }
   }
-  if (WIDE) {
-    *reinterpret_cast<float4*>(t.p + i0) = make_float4(p[0], p[1], p[2], p[3]);
+  uint8_t* mc = static_cast<uint8_t*>(t.m);
+  uint8_t* vc = static_cast<uint8_t*>(t.v);
+  float* mf = static_cast<float*>(t.m);
+  float* vf = static_cast<float*>(t.v);
+  if (wide && have == 4) {
+    __builtin_nontemporal_store(f32x4{p[0], p[1], p[2], p[3]}, reinterpret_cast<f32x4*>(t.p + i0));
     if (MX) {
-      *reinterpret_cast<uint32_t*>(mc + i0) = mw;
-      *reinterpret_cast<uint32_t*>(vc + i0) = vw;
+      __builtin_nontemporal_store(mw, reinterpret_cast<uint32_t*>(mc + i0));
+      __builtin_nontemporal_store(vw, reinterpret_cast<uint32_t*>(vc + i0));
     } else {
-      *reinterpret_cast<float4*>(mf + i0) = make_float4(m[0], m[1], m[2], m[3]);
-      *reinterpret_cast<float4*>(vf + i0) = make_float4(v[0], v[1], v[2], v[3]);
+      __builtin_nontemporal_store(f32x4{m[0], m[1], m[2], m[3]}, reinterpret_cast<f32x4*>(mf + i0));
+      __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(vf + i0));
     }
     if (t.pb)
-      *reinterpret_cast<uint2*>(t.pb + i0) =
-          make_uint2(pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]));
+      __builtin_nontemporal_store(u32x2{pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3])},
+                                  reinterpret_cast<u32x2*>(t.pb + i0));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -246,96 +358,140 @@ __device__ __forceinline__ void group4(const TensorArg& t, const Factors& f, uin
   }
 }
 
-template <bool MX>
-__device__ __forceinline__ void unit_loop(const TensorArg& t, const Factors& f, uint32_t key,
-                                          int64_t u0) {
-  const bool whole = (t.flags & kWide) && u0 + kUnit <= t.n;
-#pragma unroll 1
-  for (int s = 0; s < kSteps; ++s) {
-    const int64_t i0 = u0 + s * (kThreads * 4) + 4 * static_cast<int64_t>(threadIdx.x);
-    if (whole) {
-      group4<MX, true>(t, f, key, i0, 4);
-    } else {
-      const int64_t left = t.n - i0;
-      group4<MX, false>(t, f, key, i0, left < 0 ? 0 : (left > 4 ? 4 : static_cast<int>(left)));
-    }
+// The table is read through the scalar cache: every wave works on one tensor.
+typedef const __attribute__((address_space(4))) TensorArg* TablePtr;
+
+// The last tensor whose first unit is not behind u.
+__device__ __forceinline__ int tensor_of(const int64_t* __restrict__ units, int count, int64_t u) {
+  const int lane = lane_id();
+  int first = 0;
+  while (count > 1) {
+    const int step = (count + kWave - 1) / kWave;
+    const bool starts = lane * step < count && units[first + lane * step] <= u;
+    const int k = __popcll(__ballot(starts)) - 1;
+    first += k * step;
+    count = count - k * step < step ? count - k * step : step;
   }
+  return __builtin_amdgcn_readfirstlane(first);
 }
 
-__global__ __launch_bounds__(kThreads)
-void k_adamw(const Args a) {
-  const int lane = lane_id();
-  const uint32_t u = blockIdx.x;
-  const bool starts = lane < a.h.n_tensors && a.unit0[lane < kMaxTensors ? lane : 0] <= u;
-  const int ti = __builtin_amdgcn_readfirstlane(__popcll(__ballot(starts)) - 1);
-  const TensorArg& t = a.t[ti];
-  double lr = a.h.lr;
-  float gs = a.h.grad_scale;
-  int32_t step = a.h.step;
-  if (a.h.scalars) {
-    const mok_adamw_scalars sc = *a.h.scalars;
-    if (sc.skip != 0 || sc.step < 1) return;
+// The step's numbers, from the host or from device memory; false: nothing is done.
+__device__ __forceinline__ bool factors(const StepArg& h, float lr_scale, float weight_decay,
+                                        uint32_t number, Factors& f, uint32_t& key) {
+  double lr = h.lr;
+  f.gs = h.grad_scale;
+  int32_t step = h.step;
+  if (h.scalars) {
+    const mok_adamw_scalars sc = *h.scalars;
+    if (sc.skip != 0 || sc.step < 1) return false;
     lr = sc.lr;
-    gs = sc.grad_scale;
+    f.gs = sc.grad_scale;
     step = sc.step;
   }
+  f.b1 = static_cast<float>(h.beta1);
+  f.c1 = static_cast<float>(1.0 - h.beta1);
+  f.b2 = static_cast<float>(h.beta2);
+  f.c2 = static_cast<float>(1.0 - h.beta2);
+  lr *= static_cast<double>(lr_scale);
+  f.keep = static_cast<float>(1.0 - lr * static_cast<double>(weight_decay));
+  f.rate = static_cast<float>(lr / (1.0 - power(h.beta1, step)));
+  f.inv_bc2 = static_cast<float>(1.0 / sqrt(1.0 - power(h.beta2, step)));
+  f.eps = h.eps;
+  key = hash32(hash32(h.seed + 0x9E3779B1u * static_cast<uint32_t>(step)) + number);
+  return true;
+}
+
+template <bool MX>
+__device__ __forceinline__ void unit(const TensorArg& t, const StepArg& h, int64_t u) {
+  constexpr int kN = MX ? kMxGroups : 1;
+  const int64_t i0 = u * (kGroup * kN) + 4 * static_cast<int64_t>(threadIdx.x);
+  const bool wide = t.flags & kWide;
+  const auto have = [&](int s) {
+    const int64_t left = t.n - (i0 + s * kGroup);
+    return left < 0 ? 0 : (left > 4 ? 4 : static_cast<int>(left));
+  };
+  Group<MX> o[kN];
+#pragma unroll
+  for (int s = 0; s < kN; ++s) load<MX>(t, i0 + s * kGroup, have(s), wide, o[s]);
   Factors f;
-  lr *= static_cast<double>(t.lr_scale);
-  f.b1 = static_cast<float>(a.h.beta1);
-  f.c1 = static_cast<float>(1.0 - a.h.beta1);
-  f.b2 = static_cast<float>(a.h.beta2);
-  f.c2 = static_cast<float>(1.0 - a.h.beta2);
-  f.gs = gs;
-  f.keep = static_cast<float>(1.0 - lr * static_cast<double>(t.weight_decay));
-  f.rate = static_cast<float>(lr / (1.0 - power(a.h.beta1, step)));
-  f.inv_bc2 = static_cast<float>(1.0 / sqrt(1.0 - power(a.h.beta2, step)));
-  f.eps = a.h.eps;
-  const uint32_t key = hash32(hash32(a.h.seed + 0x9E3779B1u * static_cast<uint32_t>(step)) + t.number);
-  const int64_t u0 = static_cast<int64_t>(u - a.unit0[ti]) * kUnit;
-  if (t.flags & kMx) unit_loop<true>(t, f, key, u0);
-  else unit_loop<false>(t, f, key, u0);
+  uint32_t key;
+  if (!factors(h, t.lr_scale, t.weight_decay, t.number, f, key)) return;   // while the loads are on their way
+#pragma unroll
+  for (int s = 0; s < kN; ++s) work<MX>(t, f, key, i0 + s * kGroup, have(s), wide, o[s]);
+}
+
+template <bool MX>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, MX ? kMxWaves : kF32Waves)))
+void k_adamw(StepArg h) {
+  const int64_t u = blockIdx.x;
+  const TablePtr p = (TablePtr)(uintptr_t)(h.tensors + tensor_of(h.units, h.n_tensors, u));
+  TensorArg t;
+  t.p = p->p; t.pb = p->pb; t.g = p->g; t.m = p->m; t.v = p->v; t.ms = p->ms; t.vs = p->vs;
+  t.n = p->n; t.flags = p->flags; t.number = p->number; t.lr_scale = p->lr_scale;
+  t.weight_decay = p->weight_decay; t.unit0 = p->unit0;
+  unit<MX>(t, h, u - t.unit0);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
 
-hipError_t launch_adamw(const mok_adamw_tensor* tensors, int32_t n_tensors,
-                        const mok_adamw_hyper& h, const mok_adamw_scalars* scalars, hipStream_t s) {
-  Args a;
-  a.h = StepArg{h.lr, h.beta1, h.beta2, static_cast<float>(h.eps),
-                static_cast<float>(h.grad_scale), h.step, h.seed, scalars, 0};
-  uint32_t units = 0;
-  for (int32_t i = 0; i < n_tensors; ++i) {
-    const mok_adamw_tensor& x = tensors[i];
-    if (x.n > 0) {
-      const bool bf16 = x.grad_type == MOK_TYPE_BF16, mx = x.state_format == MOK_STATE_MXFP8;
+size_t adamw_table_bytes(int64_t n) { return descriptors_at(n) + static_cast<size_t>(n) * sizeof(TensorArg); }
+
+int64_t adamw_max_elements() { return 0x7fffffffll * kGroup; }
+
+hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* table,
+                              mok_adamw_plan& plan, hipStream_t s) {
+  int64_t* units = static_cast<int64_t*>(table);
+  TensorArg* out = reinterpret_cast<TensorArg*>(static_cast<uint8_t*>(table) + descriptors_at(n));
+  TableArg a;
+  a.first = a.count = 0;
+  plan.list = n;
+  for (int mx = 0; mx < 2; ++mx) {                      // the tensors of each format follow each other
+    const int64_t size = static_cast<int64_t>(kGroup) * (mx ? kMxGroups : 1);
+    for (int32_t i = 0; i < n; ++i) {
+      const mok_adamw_tensor& x = tensors[i];
+      if (x.n == 0 || (x.state_format == MOK_STATE_MXFP8) != (mx == 1)) continue;
+      const bool bf16 = x.grad_type == MOK_TYPE_BF16;
       const bool wide = aligned(x.p, 16) && (!x.p_bf16 || aligned(x.p_bf16, 8)) &&
                         aligned(x.grad, bf16 ? 8 : 16) && aligned(x.m, mx ? 4 : 16) &&
                         aligned(x.v, mx ? 4 : 16);
-      const int32_t at = a.h.n_tensors++;
-      a.unit0[at] = units;
-      a.t[at] = TensorArg{x.p, static_cast<uint16_t*>(x.p_bf16), x.grad, x.m, x.v, x.m_scale,
-                          x.v_scale, x.n,
-                          (bf16 ? kBf16Grad : 0) | (mx ? kMx : 0) | (wide ? kWide : 0),
-                          static_cast<uint32_t>(i), x.lr_scale, x.weight_decay};
-      units += static_cast<uint32_t>((x.n + kUnit - 1) / kUnit);
-    }
-    // a full argument, the last tensor, or a grid that the next one could push past 2^31
-    const bool full = a.h.n_tensors == kMaxTensors ||
-                      (i + 1 < n_tensors &&
-                       units + static_cast<uint64_t>((tensors[i + 1].n + kUnit - 1) / kUnit) > 0x7fffffffull);
-    if (a.h.n_tensors > 0 && (full || i + 1 == n_tensors)) {
-      hipLaunchKernelGGL(k_adamw, dim3(units), dim3(kThreads), 0, s, a);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      a.h.n_tensors = 0;
-      units = 0;
+      a.t[a.count++] = TensorArg{x.p, static_cast<uint16_t*>(x.p_bf16), x.grad, x.m, x.v, x.m_scale,
+                                 x.v_scale, x.n, (bf16 ? kBf16Grad : 0) | (wide ? kWide : 0),
+                                 static_cast<uint32_t>(i), x.lr_scale, x.weight_decay, plan.n_units[mx]};
+      plan.n_units[mx] += (x.n + size - 1) / size;
+      ++plan.n_tensors[mx];
+      if (a.count == kBatch) {
+        hipLaunchKernelGGL(k_adamw_table, dim3(1), dim3(kWave), 0, s, a, units, out);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.first += a.count;
+        a.count = 0;
+      }
     }
   }
-  return hipSuccess;
+  if (a.count == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_adamw_table, dim3(1), dim3(kWave), 0, s, a, units, out);
+  return hipGetLastError();
 }
 
-int64_t adamw_max_elements() { return 0x7fffffffll * kUnit; }
+hipError_t launch_adamw(const void* table, const mok_adamw_plan& plan, const mok_adamw_hyper& h,
+                        const mok_adamw_scalars* scalars, hipStream_t s) {
+  const int64_t* units = static_cast<const int64_t*>(table);
+  const TensorArg* t = reinterpret_cast<const TensorArg*>(static_cast<const uint8_t*>(table) + descriptors_at(plan.list));
+  StepArg a{h.lr, h.beta1, h.beta2, static_cast<float>(h.eps), static_cast<float>(h.grad_scale),
+            h.step, h.seed, scalars, units, t, plan.n_tensors[0]};
+  if (plan.n_units[0] > 0) {
+    hipLaunchKernelGGL(k_adamw<false>, dim3(static_cast<uint32_t>(plan.n_units[0])), dim3(kThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (plan.n_units[1] == 0) return hipSuccess;
+  a.units += plan.n_tensors[0];
+  a.tensors += plan.n_tensors[0];
+  a.n_tensors = plan.n_tensors[1];
+  hipLaunchKernelGGL(k_adamw<true>, dim3(static_cast<uint32_t>(plan.n_units[1])), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
 
 }  // namespace mok

@@ -152,11 +152,14 @@ hipError_t launch_route_scored_bwd(const RouterArgs& r, const void* logits, bool
 hipError_t launch_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate, float* bias,
                               bool clear_load, hipStream_t s);
 
-// AdamW over a host list of tensors (checked; none above adamw_max_elements).
-constexpr int kAdamwMaxTensors = 44;   // of one launch
+// AdamW over a list of tensors (checked; none above adamw_max_elements): the
+// table's bytes, its writing, and the step.
 int64_t adamw_max_elements();
-hipError_t launch_adamw(const mok_adamw_tensor* tensors, int32_t n_tensors,
-                        const mok_adamw_hyper& h, const mok_adamw_scalars* scalars, hipStream_t s);
+size_t adamw_table_bytes(int64_t n);
+hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* table,
+                              mok_adamw_plan& plan, hipStream_t s);
+hipError_t launch_adamw(const void* table, const mok_adamw_plan& plan, const mok_adamw_hyper& h,
+                        const mok_adamw_scalars* scalars, hipStream_t s);
 
 // The schedule counts assignments in chunks of kSchedChunk (a = t*k + j):
 // blk_counts[e][c] = local assignments to expert e in chunk c.
