@@ -257,12 +257,13 @@ __device__ __forceinline__ int count_before16(double v) {
   else return (dpp<0x120 + R>(v) > v ? 1 : 0) + count_before16<R + 1>(v);   // row_ror:R
 }
 
-// Groups before this lane's by (value, lane): for the first lane of each group;
-// the other lanes hold kNoKey.  The source of row_ror:R is below lane sl if sl >= R.
-template <int R>
-__device__ __forceinline__ int groups_before16(int rep, int own, int sl) {
-  if constexpr (R == 16) return 0;
-  else return (dpp<0x120 + R>(rep) > own - (sl >= R ? 1 : 0) ? 1 : 0) + groups_before16<R + 1>(rep, own, sl);
+// Groups before this lane's by (value, id), where every lane holds its group's
+// value and kM lanes are a group: rotations by whole groups.  The source of
+// row_ror:R is below lane sl if sl >= R.
+template <int kM, int R>
+__device__ __forceinline__ int groups_before16(int own, int sl) {
+  if constexpr (R >= 16) return 0;
+  else return (dpp<0x120 + R>(own) > own - (sl >= R ? 1 : 0) ? 1 : 0) + groups_before16<kM, R + kM>(own, sl);
 }
 
 // Whether the lane's group is among the top_groups, from values in fp64 of the
@@ -270,7 +271,7 @@ __device__ __forceinline__ int groups_before16(int rep, int own, int sl) {
 template <int kL, int V, bool BF16>
 __device__ __forceinline__ bool exact_groups(const RouterArgs& r, const Row& w, const void* __restrict__ logits,
                                              int64_t at, const float* __restrict__ bias, float top,
-                                             double inv, const int (&key)[V], int ga, int gb) {
+                                             double inv, const float (&c)[V], int ga, int gb) {
   const int lane = lane_id();
   auto score = [&](double x) {
     return r.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(top)) * inv;
@@ -278,14 +279,14 @@ __device__ __forceinline__ bool exact_groups(const RouterArgs& r, const Row& w, 
   double a = kNegInf64, b = kNegInf64;
   if (bias) {
     const float low = of_key(r.top2 && gb > kNoKey ? gb : ga);
-    const int from = key_of(low - 2.0f * (kDelta + kRel * fabsf(low)));
+    const float from = low - 2.0f * (kDelta + kRel * fabsf(low));
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i] >= from && key[i] > kNoKey) {
+      if (c[i] >= from && c[i] > kNegInf) {
         const float l = clean_logit(load_logit<BF16>(logits, at + w.first + i));
-        const double c = score(static_cast<double>(l)) + static_cast<double>(bias[w.first + i]);
-        b = c > a ? a : (c > b ? c : b);
-        a = c > a ? c : a;
+        const double x = score(static_cast<double>(l)) + static_cast<double>(bias[w.first + i]);
+        b = x > a ? a : (x > b ? x : b);
+        a = x > a ? x : a;
       }
     merge_top2(a, b, r.log_m, [](double x, double y) { return x > y ? x : y; });
   } else {                       // keys are logits: these are the two
@@ -307,7 +308,10 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
                     const float* __restrict__ bias, int32_t T, int32_t* __restrict__ idx,
                     float* __restrict__ gate, int32_t* __restrict__ load, RouteCount rc) {
   constexpr int kTok = kWave / kL;                      // tokens of a wave
-  __shared__ uint16_t slots[kWaves][kTok][kL];
+  // a candidate: its id, and for few tokens, where a second read's latency counts, its logit and bias
+  constexpr bool kCarry = kL == 64 && V <= 16;
+  using Slot = typename std::conditional<kCarry, float4, uint16_t>::type;
+  __shared__ Slot slots[kWaves][kTok][kL];
   const int lane = lane_id(), wave = threadIdx.x / kWave, sub = lane / kL;
   const Row w = row_of<kL>(r, lane);
   const int64_t t_mine = (static_cast<int64_t>(blockIdx.x) * kWaves + wave) * kTok + sub;
@@ -348,8 +352,10 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
       for (int i = 0; i < V; ++i) bv[i] = i < w.n ? bias[w.first + i] : 0.0f;
     }
   }
+  if (!(bias && r.sigmoid)) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) l[i] = clean_logit(l[i]);
+    for (int i = 0; i < V; ++i) l[i] = clean_logit(l[i]);
+  }
 
   // softmax: the row's largest logit and its sum (fp64 where the order needs it)
   float top = 0.0f;
@@ -381,29 +387,25 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
   auto softmax32 = [&](float x) { return __builtin_amdgcn_exp2f(kLog2e * (x - top)) * inv32; };
 
   // keys, and the four largest of the lane's
-  int key[V];
+  float c[V], f1 = kNegInf, f2 = kNegInf, f3 = kNegInf, f4 = kNegInf;
   if (!bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = key_of(l[i]);
-  } else if (r.sigmoid) {
+    for (int i = 0; i < V; ++i) c[i] = l[i];
+  } else if (r.sigmoid) {                    // +inf: 1, NaN and -inf: shut
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = l[i] > kNegInf ? key_of(sigmoid32(l[i]) + bv[i]) : kNoKey;
+    for (int i = 0; i < V; ++i) c[i] = l[i] > kNegInf ? sigmoid32(l[i]) + bv[i] : kNegInf;
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = l[i] > kNegInf ? key_of(softmax32(l[i]) + bv[i]) : kNoKey;
+    for (int i = 0; i < V; ++i) c[i] = l[i] > kNegInf ? softmax32(l[i]) + bv[i] : kNegInf;
   }
-  auto med3 = [](int lo, int hi, int x) {    // of lo <= hi and x
-    const int y = x > lo ? x : lo;
-    return y < hi ? y : hi;
-  };
-  int a1 = kNoKey, a2 = kNoKey, a3 = kNoKey, a4 = kNoKey;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    a4 = med3(a4, a3, key[i]);
-    a3 = med3(a3, a2, key[i]);
-    a2 = med3(a2, a1, key[i]);
-    a1 = key[i] > a1 ? key[i] : a1;
+    f4 = __builtin_amdgcn_fmed3f(f3, f4, c[i]);
+    f3 = __builtin_amdgcn_fmed3f(f2, f3, c[i]);
+    f2 = __builtin_amdgcn_fmed3f(f1, f2, c[i]);
+    f1 = c[i] > f1 ? c[i] : f1;
   }
+  int a1 = key_of(f1), a2 = key_of(f2), a3 = key_of(f3), a4 = key_of(f4);
 
   bool open = w.n > 0;
   if (r.G > 1) {
@@ -425,25 +427,25 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     }
     const bool counts = w.g < r.G && ga > kNoKey;
     const int gk = counts ? key_of(gv) : kNoKey;
-    const int rep = w.part == 0 ? gk : kNoKey;
     int before = 0;
     if constexpr (kL == 16) {
-      before = groups_before16<1>(rep, gk, w.sl);
+      if (r.log_m == 0) before = groups_before16<1, 1>(gk, w.sl);
+      else if (r.log_m == 1) before = groups_before16<2, 2>(gk, w.sl);
+      else if (r.log_m == 2) before = groups_before16<4, 4>(gk, w.sl);
+      else before = groups_before16<8, 8>(gk, w.sl);
     } else {
       for (int g = 0; g < r.G; ++g) {
-        const int o = lane_value(rep, g << r.log_m);
+        const int o = lane_value(gk, g << r.log_m);
         before += o > gk || (o == gk && g < w.g) ? 1 : 0;
       }
     }
-    // the first lane's verdict, for its group
-    const uint64_t in = __ballot(w.part == 0 && counts && before < r.top_groups);
-    bool chosen = (in >> (lane & ~((1 << r.log_m) - 1))) & 1ull;
+    bool chosen = counts && before < r.top_groups;
     if (bias || r.top2) {
       const int last = reduce<kL>(chosen ? key_of(gv - err) : 0x7fffffff, MinI());
       const int next = reduce<kL>(!chosen && counts ? key_of(gv + err) : kNoKey, MaxI());
       const bool near = next > kNoKey && next >= last;
       if (__ballot(near)) {
-        const bool sure = exact_groups<kL, V, BF16>(r, w, logits, at, bias, top, inv, key, ga, gb);
+        const bool sure = exact_groups<kL, V, BF16>(r, w, logits, at, bias, top, inv, c, ga, gb);
         chosen = near ? sure : chosen;
       }
     }
@@ -466,19 +468,18 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     const float f = of_key(t0);
     thr = key_of(f - 2.0f * (kDelta + kRel * fabsf(f)));
   }
-  thr = thr > kNoKey ? thr : kNoKey + 1;                // every eligible expert, where k are not there
-  if (!open) thr = 0x7fffffff;
+  // every eligible expert, where k are not there (the lowest finite value); none of a shut group
+  const float from = open ? of_key(thr > kNoKey ? thr : kNoKey + 1) : __builtin_inff();
 
   // candidates, in id order
-  using Bits = typename std::conditional<V <= 32, uint32_t, uint64_t>::type;
-  Bits bits = 0;
+  uint32_t bits = 0;                                    // kL = 16: element i at bit V - 1 - i
   int have = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    if (V <= 64) bits |= key[i] >= thr ? Bits{1} << (i & (8 * sizeof(Bits) - 1)) : Bits{0};
-    else have += key[i] >= thr ? 1 : 0;
+    if constexpr (kL == 16) bits = bits + bits + (c[i] >= from ? 1u : 0u);
+    else have += c[i] >= from ? 1 : 0;
   }
-  if (V <= 64) have = __popcll(bits);
+  if constexpr (kL == 16) have = __popc(bits);
   int slot = have;                                      // inclusive prefix over the token's lanes
   slot += dpp<0x111>(slot);                             // row_shr:1, 2, 4, 8 (0 from outside)
   slot += dpp<0x112>(slot);
@@ -494,19 +495,23 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     n_cand = lane_value(slot, 63);
   }
   slot -= have;
-  uint16_t* mine = slots[wave][sub];
-  if constexpr (V <= 64) {
+  Slot* mine = slots[wave][sub];
+  if constexpr (kL == 16) {
+    bits <<= 32 - V;                                    // the lowest id at the top
     while (bits) {
-      const int i = __ffsll(static_cast<unsigned long long>(bits)) - 1;
-      bits &= bits - 1;
+      const int i = __clz(static_cast<int>(bits));
+      bits &= ~(0x80000000u >> i);
       if (slot < kL) mine[slot] = static_cast<uint16_t>(w.first + i);
       ++slot;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i] >= thr) {
-        if (slot < kL) mine[slot] = static_cast<uint16_t>(w.first + i);
+      if (c[i] >= from) {
+        if (slot < kL) {
+          if constexpr (kCarry) mine[slot] = make_float4(l[i], bias ? bv[i] : 0.0f, __int_as_float(w.first + i), 0.0f);
+          else mine[slot] = static_cast<uint16_t>(w.first + i);
+        }
         ++slot;
       }
   }
@@ -516,19 +521,30 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
 
   // fp64 values of the candidates, one to a lane, and their places
   int e = -1, place = w.sl;
-  float le = kNegInf;
+  float le = kNegInf, be = 0.0f;
   double s = 0.0;
-  auto score64 = [&]() {
+  const auto read = [&]() {                 // the logit and bias of expert e
     le = e >= 0 ? clean_logit(load_logit<BF16>(logits, at + e)) : kNegInf;
+    be = bias && e >= 0 ? bias[e] : 0.0f;
+  };
+  const auto score64 = [&]() {
     s = 0.0;
     if (e >= 0)
       s = r.sigmoid ? sigmoid64(le) : exp(static_cast<double>(le) - static_cast<double>(top)) * inv;
   };
-  if (!plain && w.sl < n_cand) e = mine[w.sl];
+  if constexpr (!kCarry) {
+    if (!plain && w.sl < n_cand) e = mine[w.sl];
+    read();
+  } else if (!plain && w.sl < n_cand) {
+    const float4 q = mine[w.sl];
+    le = clean_logit(q.x);
+    be = q.y;
+    e = __float_as_int(q.z);
+  }
   score64();
   {
     double v = kNegInf64;
-    if (e >= 0) v = bias ? s + static_cast<double>(bias[e]) : static_cast<double>(le);
+    if (e >= 0) v = bias ? s + static_cast<double>(be) : static_cast<double>(le);
     // equal values in id order, which is lane order: the lane's number in the last bits (the larger
     // value for the lower lane, of either sign)
     if (e >= 0) {
@@ -549,6 +565,7 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     if (plain) {
       e = pe;
       place = w.sl;
+      read();
       score64();
     }
   }
