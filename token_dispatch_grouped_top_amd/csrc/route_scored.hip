@@ -7,10 +7,10 @@
 // over 256 experts about ten have two neighbours in their order within fp32's
 // error).  An fp64 exponential of every logit costs more than all the rest,
 // so a token's experts go through two steps:
-//   1. fp32 keys (c with an error below kDelta; without a bias the logits
+//   1. fp32 keys (c with a known error; without a bias the logits
 //      themselves, whose order is the scores') find a value t0 that at least k
 //      experts reach, and the candidates are those with a key of at least
-//      t0 - 2 kDelta: all that could be among the k largest c, seldom more than
+//      t0 less twice the error: all that could be among the k largest c, seldom more than
 //      k + 1;
 //   2. the candidates, one to a lane, get c in fp64, and each counts the
 //      candidates before it, which is its place among the picks.
@@ -37,16 +37,20 @@ namespace {
 constexpr int kWaves = 4;
 constexpr float kNegInf = -__builtin_inff();
 constexpr double kNegInf64 = -__builtin_inf();
-// Error of an fp32 key: s = 1 / (1 + 2^(-x log2 e)) with one step (2^-23) each
-// of the exponential and the reciprocal and |x| 2^-23 of the exponent, of which
-// s (1 - s) <= 1/4 and |x| s (1 - s) <= 0.23 reach s: below 2^-22 (softmax: the
-// same of e^x <= 1, x e^x <= 0.37, with its sum's reciprocal: below 2^-21); the
-// sum with the bias adds 2^-24 of itself (kRel, doubled).
-constexpr float kDelta = 0x1p-21f;
+// Error of an fp32 key.  Sigmoid, s = 1 / (1 + 2^(-x log2 e)): of e^-x the
+// relative error |x| 1.25 2^-24 (the exponent) + 2^-23 (its power), of which
+// s (1 - s) <= 1/4 and |x| s (1 - s) <= 0.23 reach s, of the sum and its
+// reciprocal 1.5 2^-23: below 1.9 2^-23.  Softmax: |x| 2.25 2^-24 + 2^-22 of
+// p <= 1, with p |x| <= 0.37: below 2.5 2^-23.  The sum with the bias adds 2^-24
+// of itself (kRel, doubled).
+constexpr float kSigmoidErr = 0x1p-22f, kSoftmaxErr = 0x1p-21f;
 constexpr float kRel = 0x1p-23f;
 constexpr float kLog2e = 1.44269504f;
-// Tokens from which four share a wave.
-constexpr int kManyTokens = 2048;
+// Tokens from which four share a wave: forward (384 experts, 16 against 64 lanes
+// a token: 2048 tokens 4.6 and 4.7 us, 16384 9.5 and 17.2), sparse backward (256
+// experts in bf16: 4096 tokens 3.5 and 3.35 us, 16384 4.8 and 7.0), dense
+// backward (16384 10.3 and 9.4 us, 65536 29.0 and 27.6; 160 experts 21.7 and 25.8).
+constexpr int kManyTokens = 2048, kManySparse = 8192, kManyDense = 32768;
 // Picks up to which each adds to the load by itself.
 constexpr int kDirectPicks = 2048;
 
@@ -279,15 +283,23 @@ __device__ __forceinline__ bool exact_groups(const RouterArgs& r, const Row& w, 
   double a = kNegInf64, b = kNegInf64;
   if (bias) {
     const float low = of_key(r.top2 && gb > kNoKey ? gb : ga);
-    const float from = low - 2.0f * (kDelta + kRel * fabsf(low));
+    const float from = low - 2.0f * ((r.sigmoid ? kSigmoidErr : kSoftmaxErr) + kRel * fabsf(low));
+    // a lane's few, one a turn (the largest V in passes of 32)
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c[i] >= from && c[i] > kNegInf) {
-        const float l = clean_logit(load_logit<BF16>(logits, at + w.first + i));
-        const double x = score(static_cast<double>(l)) + static_cast<double>(bias[w.first + i]);
+    for (int i0 = 0; i0 < V; i0 += 32) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int i = i0; i < V && i < i0 + 32; ++i)
+        if (c[i] >= from && c[i] > kNegInf) bits |= 1u << (i - i0);
+      while (bits) {
+        const int e = w.first + i0 + __ffs(static_cast<int>(bits)) - 1;
+        bits &= bits - 1;
+        const double x = score(static_cast<double>(clean_logit(load_logit<BF16>(logits, at + e)))) +
+                         static_cast<double>(bias[e]);
         b = x > a ? a : (x > b ? x : b);
         a = x > a ? x : a;
       }
+    }
     merge_top2(a, b, r.log_m, [](double x, double y) { return x > y ? x : y; });
   } else {                       // keys are logits: these are the two
     if (ga > kNoKey) a = score(static_cast<double>(of_key(ga)));
@@ -407,12 +419,13 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
   }
   int a1 = key_of(f1), a2 = key_of(f2), a3 = key_of(f3), a4 = key_of(f4);
 
+  const float delta = r.sigmoid ? kSigmoidErr : kSoftmaxErr;
   bool open = w.n > 0;
   if (r.G > 1) {
     int ga = a1, gb = a2;
     merge_top2(ga, gb, r.log_m, MaxI());
     const float fa = of_key(ga);
-    float gv = fa, err = bias ? kDelta + kRel * fabsf(fa) : 0.0f;
+    float gv = fa, err = bias ? delta + kRel * fabsf(fa) : 0.0f;
     if (r.top2) {
       float fb = of_key(gb);
       if (!bias) {               // keys are logits: the sum is of scores
@@ -420,7 +433,7 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
         fb = gb > kNoKey ? (r.sigmoid ? sigmoid32(fb) : softmax32(fb)) : kNegInf;
       }
       if (gb > kNoKey) gv += fb;
-      err = 2.0f * kDelta + 2.0f * kRel * (bias ? fabsf(fa) + (gb > kNoKey ? fabsf(fb) : 0.0f) : gv);
+      err = 2.0f * delta + 2.0f * kRel * (bias ? fabsf(fa) + (gb > kNoKey ? fabsf(fb) : 0.0f) : gv);
       // without a bias the relative error counts too, below 2^-16 for |x| < 104 (and 2^-120 for
       // exponentials that leave the normal numbers)
       if (!bias) err = fminf(err, 0x1p-16f * gv) + 0x1p-120f;
@@ -466,7 +479,7 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
   int thr = t0;
   if (bias && t0 > kNoKey) {
     const float f = of_key(t0);
-    thr = key_of(f - 2.0f * (kDelta + kRel * fabsf(f)));
+    thr = key_of(f - 2.0f * (delta + kRel * fabsf(f)));
   }
   // every eligible expert, where k are not there (the lowest finite value); none of a shut group
   const float from = open ? of_key(thr > kNoKey ? thr : kNoKey + 1) : __builtin_inff();
@@ -904,7 +917,7 @@ hipError_t launch_route_scored_bwd(const RouterArgs& r, const void* logits, bool
   if (T == 0) return hipSuccess;
   const int E = r.E;
   const bool dense = !r.sigmoid && !r.renorm;
-  if (T >= kManyTokens && r.k <= 16 && E <= 512) {      // four tokens to a wave
+  if (T >= (dense ? kManyDense : kManySparse) && r.k <= 16 && E <= 512) {   // four tokens to a wave
     if (!dense) return launch_bwd_v<16, 0>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
     if (E <= 64) return launch_bwd_v<16, 4>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
     if (E <= 128) return launch_bwd_v<16, 8>(r, logits, bf16, ld, T, idx, dgate, dlogits, ldd, s);
