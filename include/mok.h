@@ -192,7 +192,8 @@ typedef struct {
  * differ by less than 2^-48 of them, and not by nothing, may come in either
  * order.
  * load (int32 [E], or NULL): the number of tokens that picked each expert is
- * added to it. */
+ * added to it.  Every pointer is aligned for its elements.  T up to 2^26 - 4
+ * (MOK_ERR_UNSUPPORTED), here and in the two calls that follow from it. */
 mok_status mok_route_scored(const mok_router_desc* router, const void* logits, int32_t logits_type,
                             int64_t ld, const float* bias, int32_t T, int32_t* topk_idx,
                             float* topk_gate, int32_t* load, hipStream_t stream);
@@ -219,8 +220,8 @@ mok_status mok_route_scored_backward(const mok_router_desc* router, const void* 
  * once (load: int32 [n_layers][E], not negative; bias: fp32 [n_layers][E]):
  *   bias[l][e] += rate * sign(sum_i load[l][i] - E * load[l][e])
  * (the sign from 64-bit integers), so that experts below the mean load are
- * picked more often.  clear_load != 0: load is zero afterwards.  E up to
- * 65536. */
+ * picked more often.  clear_load = 1: load is zero afterwards.  E up to 65536,
+ * n_layers below 2^22 (MOK_ERR_UNSUPPORTED). */
 mok_status mok_route_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate,
                                  float* bias, int32_t clear_load, hipStream_t stream);
 
@@ -675,7 +676,8 @@ typedef struct {
  * the host keeps (private to the library).  Table and plan serve any number of
  * steps, on any stream that comes after the writing, as long as the tensors
  * stay where they are.  No two buffers that a step writes may overlap;
- * overlapping p are refused (MOK_ERR_INVALID_ARG).  fp32 pointers must be
+ * overlapping p are refused (MOK_ERR_INVALID_ARG), and so are lists of more than
+ * 2^24 units of 1024 elements (MOK_ERR_UNSUPPORTED).  fp32 pointers must be
  * 4-byte, bf16 pointers 2-byte aligned; tensors whose pointers are all aligned
  * for 4 elements (16 bytes of fp32) go faster. */
 typedef struct {

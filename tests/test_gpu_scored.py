@@ -70,6 +70,7 @@ ROUTES = [
     (8, 2, 1, 1, False), (1, 1, 1, 1, False), (7, 7, 1, 1, False), (33, 5, 1, 1, False), (64, 8, 8, 3, True),
     (160, 6, 8, 3, False), (256, 8, 8, 4, True), (384, 8, 1, 1, False), (65, 4, 5, 2, True), (63, 9, 21, 4, True),
     (60, 3, 60, 7, True), (1000, 32, 4, 2, False), (513, 12, 27, 9, True), (2048, 16, 64, 5, True), (4096, 32, 2, 1, False),
+    (4095, 8, 3, 2, True), (4092, 6, 33, 5, True),
 ]
 
 
@@ -127,6 +128,51 @@ def test_route_of_many_tokens(E, k, G, top_groups, top2, score):
         err = np.abs(gate.cpu().numpy().astype(np.float64) - rg)
         assert np.all(err <= _gate_bar(lv, rg)), (kind, dtype, err.max())
         assert np.array_equal(load.cpu().numpy(), rl)
+
+
+@pytest.mark.parametrize("T", [70, 2100])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_buffers_at_any_element(T, dtype):
+    """Logits, gradients and bias that begin one element behind an aligned address, rows that keep the alignment."""
+    rng = np.random.default_rng(T)
+    E, k = 64, 6
+    r = _router(E, k, ref.SIGMOID, 4, 2, True, True, 2.5)
+    r_dense = _router(E, k, ref.SOFTMAX)
+    store = torch.from_numpy(rng.normal(size=(T, E + 8))).to(dtype).cuda()
+    x, bias = store[:, 1:E + 1], (0.1 * torch.randn(E + 1, device="cuda"))[1:]
+    idx = torch.full((T * k + 1,), 9, dtype=torch.int32, device="cuda")[1:]
+    gate = torch.empty(T * k + 1, device="cuda")[1:]
+    mok.mok_route_scored(r, x, T, idx, gate, bias=bias)
+    lv = x.double().cpu().numpy()
+    ri, rg, _ = ref.route(lv, ref.SIGMOID, k, bias.cpu().numpy(), 4, 2, True, True, 2.5)
+    assert np.array_equal(idx.view(T, k).cpu().numpy(), ri)
+    assert np.all(np.abs(gate.view(T, k).double().cpu().numpy() - rg) <= _gate_bar(lv, rg))
+    dg = torch.randn(T * k + 1, device="cuda")[1:]
+    for router, score, renorm, scale in ((r, ref.SIGMOID, True, 2.5), (r_dense, ref.SOFTMAX, False, 1.0)):
+        out = torch.full((T, E + 8), 3.0, dtype=dtype, device="cuda")
+        mok.mok_route_scored_backward(router, x, T, idx, dg, out[:, 1:E + 1])
+        want, size = ref.route_backward(lv, score, ri, dg.view(T, k).double().cpu().numpy(), renorm, scale)
+        bar = (4 * 10 + 192) * 2.0 ** -24 * size + 2.0 ** -120
+        if dtype == torch.bfloat16:
+            bar = bar + 2.0 ** -8 * (np.abs(want) + bar)
+        assert np.all(np.abs(out[:, 1:E + 1].double().cpu().numpy() - want) <= bar)
+        assert bool((out[:, 0] == 3.0).all()) and bool((out[:, E + 1:] == 3.0).all())
+
+
+def test_two_streams_add_to_one_load():
+    """Two calls at once on different streams, their loads counted into one buffer."""
+    E, k, T = 96, 4, 3000
+    r = _router(E, k, ref.SOFTMAX)
+    load = torch.zeros(E, dtype=torch.int32, device="cuda")
+    xs = [torch.randn(T, E, device="cuda") for _ in range(2)]
+    outs = [(torch.empty(T, k, dtype=torch.int32, device="cuda"), torch.empty(T, k, device="cuda")) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, x, (i, g) in zip(streams, xs, outs):
+        mok.mok_route_scored(r, x, T, i, g, load=load, stream=s)
+    torch.cuda.synchronize()
+    want = sum(ref.route(x.double().cpu().numpy(), ref.SOFTMAX, k)[2] for x in xs)
+    assert np.array_equal(load.cpu().numpy(), want)
 
 
 def test_route_tells_close_scores_apart():

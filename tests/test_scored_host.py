@@ -46,6 +46,16 @@ def test_route_refusals():
     assert route(r, 16, 0, 32, None, 4, None, 16, None, None) == E_ARG
     assert route(r, 16, 0, 32, None, 4, 16, None, None, None) == E_ARG
     assert route(r, None, 0, 32, None, 0, None, None, None, None) == mok.MOK_OK   # no tokens
+    assert route(r, 18, 0, 32, None, 4, 16, 16, None, None) == E_ARG      # fp32 at no multiple of 4
+    assert route(r, 17, 1, 32, None, 4, 16, 16, None, None) == E_ARG      # bf16 at an odd address
+    assert route(r, 16, 0, 32, 18, 4, 16, 16, None, None) == E_ARG
+    assert route(r, 16, 0, 32, None, 4, 18, 16, None, None) == E_ARG
+    assert route(r, 16, 0, 32, None, 4, 16, 18, None, None) == E_ARG
+    assert route(r, 16, 0, 32, None, 4, 16, 16, 18, None) == E_ARG
+    assert route(r, 16, 0, 32, None, 1 << 26, 16, 16, None, None) == E_UNS   # more threads than a launch has
+    assert bwd(r, 16, 0, 32, 1 << 26, 16, 16, 16, 32, None) == E_UNS
+    assert bwd(r, 18, 0, 32, 4, 16, 16, 16, 32, None) == E_ARG
+    assert bwd(r, 16, 1, 32, 4, 16, 16, 17, 32, None) == E_ARG
     assert bwd(r, 16, 0, 32, 4, 16, 16, 16, 31, None) == E_ARG            # ldd < E
     assert bwd(r, 16, 0, 32, 4, None, 16, 16, 32, None) == E_ARG
     assert bwd(r, 16, 0, 32, 4, 16, None, 16, 32, None) == E_ARG
@@ -60,6 +70,8 @@ def test_route_refusals():
     assert bias(None, 1, 8, 1e-3, 16, 0, None) == E_ARG
     assert bias(16, 1, 8, 1e-3, None, 0, None) == E_ARG
     assert bias(None, 0, 8, 1e-3, None, 0, None) == mok.MOK_OK
+    assert bias(18, 1, 8, 1e-3, 16, 0, None) == E_ARG and bias(16, 1, 8, 1e-3, 18, 0, None) == E_ARG
+    assert bias(16, 1 << 22, 8, 1e-3, 16, 0, None) == E_UNS
 
 
 def test_forward_scored_refusals():
@@ -75,6 +87,7 @@ def test_forward_scored_refusals():
     assert go(router=_router(top_groups=0)) == E_ARG
     assert go(logits=None) == E_ARG
     assert go(kind=3) == E_ARG
+    assert go(logits=18) == E_ARG and go(idx=18) == E_ARG
     assert go(ld=31) == E_ARG
     assert go(idx=None) == E_ARG and go(gate=None) == E_ARG                # both or neither
     assert go(T=17) == E_ARG                                               # more tokens than rows
@@ -108,7 +121,7 @@ def test_adamw_table_refusals():
     assert _build([t, t]) == E_ARG                                         # the same tensor twice
     assert _build([t, _tensor(p=(1 << 20) + 64 * 4 - 4)]) == E_ARG         # overlapping parameters
     assert _build([_tensor(n=1 << 62)]) == E_UNS
-    far = [_tensor(p=i << 50, n=1 << 40) for i in range(1, 4)]             # more units than a launch has
+    far = [_tensor(p=i << 50, n=6 << 30) for i in range(1, 4)]             # more units than a launch has
     assert _build(far) == E_UNS
     assert _build([t], table=None) == E_ARG
     assert _build([t], table=72) == E_ARG                                  # not 16-byte aligned
@@ -137,7 +150,7 @@ def test_adamw_step_refusals():
     assert step(scalars=8) == E_ARG                                        # not 16-byte aligned
     assert step(table=None) == E_ARG
     for plan in (dict(n_units=(-1, 0)), dict(n_units=(1, 0)), dict(n_units=(0, 1), n_tensors=(1, 0), list=1),
-                 dict(n_units=(0, 1 << 31), n_tensors=(0, 1), list=1), dict(n_units=(1, 0), n_tensors=(-1, 0)),
+                 dict(n_units=(0, 1 << 24), n_tensors=(0, 1), list=1), dict(n_units=(1, 0), n_tensors=(-1, 0)),
                  dict(n_units=(1, 0), n_tensors=(2, 0), list=1), dict(n_units=(1, 1), n_tensors=(1, 1), list=1)):
         assert step(plan=plan) == E_ARG, plan
     assert step(plan={}, table=None) == mok.MOK_OK                         # an empty list

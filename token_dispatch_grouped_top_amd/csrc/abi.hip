@@ -196,6 +196,15 @@ RouterArgs router_args(const mok_router_desc* r) {
 
 bool type_ok(int32_t t) { return t == MOK_TYPE_F32 || t == MOK_TYPE_BF16; }
 
+// Whether p is no multiple of the type's size (null is one).
+bool odd(const void* p, size_t size) { return reinterpret_cast<uintptr_t>(p) % size != 0; }
+size_t type_size(int32_t t) { return t == MOK_TYPE_BF16 ? 2 : 4; }
+
+// A launch has fewer than 2^32 threads: tokens at one wave each, layers of the
+// bias update at 1024 threads.
+constexpr int32_t kMaxRouteTokens = (1 << 26) - 4;
+constexpr int32_t kMaxBiasLayers = (1 << 22) - 1;
+
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
 mok_status hip_status(hipError_t e) {
@@ -237,6 +246,10 @@ mok_status mok_route_scored(const mok_router_desc* router, const void* logits, i
   if (!router_ok(router) || !type_ok(logits_type) || T < 0 || ld < router->n_experts)
     return MOK_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_idx || !topk_gate)) return MOK_ERR_INVALID_ARG;
+  if (odd(logits, type_size(logits_type)) || odd(bias, 4) || odd(topk_idx, 4) || odd(topk_gate, 4) ||
+      odd(load, 4))
+    return MOK_ERR_INVALID_ARG;
+  if (T > kMaxRouteTokens) return MOK_ERR_UNSUPPORTED;
   return hip_status(launch_route_scored(router_args(router), logits, logits_type == MOK_TYPE_BF16,
                                         ld, bias, T, topk_idx, topk_gate, load, RouteCount{},
                                         stream));
@@ -250,6 +263,10 @@ mok_status mok_route_scored_backward(const mok_router_desc* router, const void* 
       ldd < router->n_experts)
     return MOK_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_idx || !dgate || !dlogits)) return MOK_ERR_INVALID_ARG;
+  if (odd(logits, type_size(logits_type)) || odd(dlogits, type_size(logits_type)) ||
+      odd(topk_idx, 4) || odd(dgate, 4))
+    return MOK_ERR_INVALID_ARG;
+  if (T > kMaxRouteTokens) return MOK_ERR_UNSUPPORTED;
   return hip_status(launch_route_scored_bwd(router_args(router), logits,
                                             logits_type == MOK_TYPE_BF16, ld, T, topk_idx, dgate,
                                             dlogits, ldd, stream));
@@ -260,6 +277,8 @@ mok_status mok_route_bias_update(int32_t* load, int32_t n_layers, int32_t E, flo
   if (n_layers < 0 || E < 1 || E > 65536 || !std::isfinite(rate)) return MOK_ERR_INVALID_ARG;
   if (clear_load != 0 && clear_load != 1) return MOK_ERR_INVALID_ARG;
   if (n_layers > 0 && (!load || !bias)) return MOK_ERR_INVALID_ARG;
+  if (odd(load, 4) || odd(bias, 4)) return MOK_ERR_INVALID_ARG;
+  if (n_layers > kMaxBiasLayers) return MOK_ERR_UNSUPPORTED;
   return hip_status(launch_bias_update(load, n_layers, E, rate, bias, clear_load != 0, stream));
 }
 
@@ -288,8 +307,7 @@ mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tens
       const bool mx = x.state_format == MOK_STATE_MXFP8;
       if (!x.p || !x.grad || !x.m || !x.v || (mx && (!x.m_scale || !x.v_scale)))
         return MOK_ERR_INVALID_ARG;
-      auto odd = [](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a != 0; };
-      if (odd(x.p, 4) || odd(x.p_bf16, 2) || odd(x.grad, x.grad_type == MOK_TYPE_BF16 ? 2 : 4) ||
+      if (odd(x.p, 4) || odd(x.p_bf16, 2) || odd(x.grad, type_size(x.grad_type)) ||
           (!mx && (odd(x.m, 4) || odd(x.v, 4))))
         return MOK_ERR_INVALID_ARG;
       const uintptr_t at = reinterpret_cast<uintptr_t>(x.p);
@@ -301,7 +319,7 @@ mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tens
   } catch (const std::bad_alloc&) {
     return MOK_ERR_UNSUPPORTED;
   }
-  if (units > 0x7fffffff) return MOK_ERR_UNSUPPORTED;      // one launch's grid
+  if (units > kAdamwMaxUnits) return MOK_ERR_UNSUPPORTED;   // one launch's grid
   if (n_tensors > 0 && table_bytes < adamw_table_bytes(n_tensors)) return MOK_ERR_WORKSPACE;
   *plan = mok_adamw_plan{};
   return hip_status(launch_adamw_table(tensors, n_tensors, table, *plan, stream));
@@ -312,7 +330,7 @@ mok_status mok_adamw_step(const void* table, const mok_adamw_plan* plan,
                           hipStream_t stream) {
   if (!plan || !hyper) return MOK_ERR_INVALID_ARG;
   for (int i = 0; i < 2; ++i)
-    if (plan->n_units[i] < 0 || plan->n_units[i] > 0x7fffffff || plan->n_tensors[i] < 0 ||
+    if (plan->n_units[i] < 0 || plan->n_units[i] > kAdamwMaxUnits || plan->n_tensors[i] < 0 ||
         (plan->n_units[i] > 0 && (plan->n_tensors[i] < 1 || !table)))
       return MOK_ERR_INVALID_ARG;
   if (plan->list < static_cast<int64_t>(plan->n_tensors[0]) + plan->n_tensors[1])
@@ -1128,8 +1146,10 @@ mok_status mok_moe_forward_scored(const mok_layer_desc* desc, const mok_router_d
                                   hipStream_t stream) {
   if (!desc || !router_ok(router) || router->n_experts != desc->n_experts ||
       router->top_k != desc->top_k || !type_ok(logits_type) || ld < router->n_experts ||
-      (T > 0 && !logits) || !topk_idx != !topk_gate)
+      (T > 0 && !logits) || !topk_idx != !topk_gate || odd(logits, type_size(logits_type)) ||
+      odd(bias, 4) || odd(topk_idx, 4) || odd(topk_gate, 4) || odd(load, 4))
     return MOK_ERR_INVALID_ARG;
+  if (T > kMaxRouteTokens) return MOK_ERR_UNSUPPORTED;
   const mok::ScoredRoute sr{router_args(router), logits, logits_type == MOK_TYPE_BF16, ld, bias,
                             topk_idx, topk_gate, load};
   return mok::forward_impl(desc, 1, nullptr, nullptr, nullptr, nullptr, T, x, w_gate_up, w_down,

@@ -438,7 +438,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 size_t adamw_table_bytes(int64_t n) { return descriptors_at(n) + static_cast<size_t>(n) * sizeof(TensorArg); }
 
-int64_t adamw_max_elements() { return 0x7fffffffll * kGroup; }
+int64_t adamw_max_elements() { return kAdamwMaxUnits * kGroup; }
 
 hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* table,
                               mok_adamw_plan& plan, hipStream_t s) {

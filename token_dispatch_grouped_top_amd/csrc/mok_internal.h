@@ -154,6 +154,7 @@ hipError_t launch_bias_update(int32_t* load, int32_t n_layers, int32_t E, float 
 
 // AdamW over a list of tensors (checked; none above adamw_max_elements): the
 // table's bytes, its writing, and the step.
+constexpr int64_t kAdamwMaxUnits = (1 << 24) - 1;   // workgroups of a launch (2^32 threads)
 int64_t adamw_max_elements();
 size_t adamw_table_bytes(int64_t n);
 hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* table,

@@ -605,7 +605,7 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
 // The load of many picks: a workgroup counts its share in LDS and adds each
 // expert's count once.  (One atomic for each pick costs about 1 ns, all of them
 // on the same few lines: 131072 picks of 256 experts 130 us.)
-constexpr int kLoadThreads = 1024, kLoadPicks = 8 * kLoadThreads;
+constexpr int kLoadThreads = 1024, kLoadPicks = 4 * kLoadThreads;
 
 __global__ __launch_bounds__(kLoadThreads)
 void k_load_count(const int32_t* __restrict__ idx, int64_t n, int32_t E, int32_t* __restrict__ load) {
