@@ -167,11 +167,13 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(ValueError, match="logits"):
             mok.mok_route_scored(r, bad, 4, idx, gate, stream=0)
     with pytest.raises(ValueError, match="topk_idx"):
-        mok._buffer(idx.long(), "topk_idx", (torch.int32,), 16)
+        mok._buffer(idx.long(), "topk_idx", (torch.int32,), 16, 0)
     with pytest.raises(ValueError, match="topk_idx"):
-        mok._buffer(idx, "topk_idx", (torch.int32,), 17)
+        mok._buffer(idx, "topk_idx", (torch.int32,), 17, 0)
     with pytest.raises(ValueError, match="topk_idx"):
-        mok._buffer(idx.t(), "topk_idx", (torch.int32,), 16)
+        mok._buffer(idx.t(), "topk_idx", (torch.int32,), 16, 0)
+    with pytest.raises(ValueError, match="topk_idx.*current GPU"):
+        mok._buffer(idx, "topk_idx", (torch.int32,), 16, 0)
     f = torch.zeros(64)
     for t in (dict(p=f, grad=f, m=f, v=f), dict(p=f.double(), grad=f, m=f, v=f),
               dict(p=f, grad=f.half(), m=f, v=f)):

@@ -229,9 +229,14 @@ def mok_route_topk(logits, T: int, E: int, k: int, topk_idx, topk_gate, stream=N
 _TYPES = {torch.float32: MOK_TYPE_F32, torch.bfloat16: MOK_TYPE_BF16}
 
 
-def _buffer(x, name: str, dtypes, n: int) -> int:
+def _device() -> int:
+    """The current GPU, -1 before torch has touched one."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+
+
+def _buffer(x, name: str, dtypes, n: int, device: int) -> int:
     """Address of a buffer of at least n elements: None, a raw address (not checked), or a dense
-    tensor of one of dtypes on the current GPU."""
+    tensor of one of dtypes on the GPU `device`."""
     if x is None or isinstance(x, int):
         return x or 0
     if x.dtype not in dtypes:
@@ -239,58 +244,61 @@ def _buffer(x, name: str, dtypes, n: int) -> int:
     if not x.is_contiguous() or x.numel() < n:
         raise ValueError(f"{name}: {tuple(x.shape)} with strides {x.stride()} where {n} dense elements "
                          "are wanted")
-    return _on_device(x, name)
-
-
-def _on_device(x, name: str) -> int:
-    device = x.get_device()
-    if device < 0 or device != torch._C._cuda_getDevice():
+    if x.get_device() != device or device < 0:
         raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
     return x.data_ptr()
 
 
-def _rows(x, name: str, T: int, E: int):
+def _rows(x, name: str, T: int, E: int, device: int):
     """(address, mok_type, row stride) of fp32 or bf16 rows, the rows themselves dense."""
     if x is None:
         return 0, MOK_TYPE_F32, E
-    if x.dtype not in _TYPES:
+    kind = _TYPES.get(x.dtype)
+    if kind is None:
         raise ValueError(f"{name}: {x.dtype} where torch.float32 or torch.bfloat16 is wanted")
-    if x.dim() != 2 or x.shape[0] < T or x.shape[1] != E or (E > 1 and x.stride(1) != 1):
-        raise ValueError(f"{name}: {tuple(x.shape)} with strides {x.stride()} where [{T}][{E}] rows of "
+    shape, (ld, step) = x.shape, x.stride() if x.dim() == 2 else (0, 0)
+    if ld == 0 and step == 0 or shape[0] < T or shape[1] != E or (E > 1 and step != 1):
+        raise ValueError(f"{name}: {tuple(shape)} with strides {x.stride()} where [{T}][{E}] rows of "
                          "dense values are wanted")
-    return _on_device(x, name), _TYPES[x.dtype], x.stride(0) if T > 1 else max(x.stride(0), E)
+    if x.get_device() != device or device < 0:
+        raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
+    return x.data_ptr(), kind, ld if T > 1 else max(ld, E)
+
+
+_F32, _I32S, _U8, _BF16 = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.bfloat16,)
 
 
 def mok_route_scored(router: mok_router_desc, logits, T: int, topk_idx, topk_gate, bias=None,
                      load=None, stream=None) -> None:
-    E, n = router.n_experts, T * router.top_k
-    at, kind, ld = _rows(logits, "logits", T, E)
+    E, n, device = router.n_experts, T * router.top_k, _device()
+    at, kind, ld = _rows(logits, "logits", T, E, device)
     _check(_lib.mok_route_scored(C.byref(router), at, kind, ld,
-                                 _buffer(bias, "bias", (torch.float32,), E), T,
-                                 _buffer(topk_idx, "topk_idx", (torch.int32,), n),
-                                 _buffer(topk_gate, "topk_gate", (torch.float32,), n),
-                                 _buffer(load, "load", (torch.int32,), E), _stream(stream)),
+                                 _buffer(bias, "bias", _F32, E, device), T,
+                                 _buffer(topk_idx, "topk_idx", _I32S, n, device),
+                                 _buffer(topk_gate, "topk_gate", _F32, n, device),
+                                 _buffer(load, "load", _I32S, E, device), _stream(stream)),
            "mok_route_scored")
 
 
 def mok_route_scored_backward(router: mok_router_desc, logits, T: int, topk_idx, dgate, dlogits,
                               stream=None) -> None:
-    E, n = router.n_experts, T * router.top_k
-    at, kind, ld = _rows(logits, "logits", T, E)
-    to, kind_to, ldd = _rows(dlogits, "dlogits", T, E)
+    E, n, device = router.n_experts, T * router.top_k, _device()
+    at, kind, ld = _rows(logits, "logits", T, E, device)
+    to, kind_to, ldd = _rows(dlogits, "dlogits", T, E, device)
     if kind_to != kind:
         raise ValueError(f"dlogits: {dlogits.dtype} where the logits are {logits.dtype}")
     _check(_lib.mok_route_scored_backward(C.byref(router), at, kind, ld, T,
-                                          _buffer(topk_idx, "topk_idx", (torch.int32,), n),
-                                          _buffer(dgate, "dgate", (torch.float32,), n), to, ldd,
+                                          _buffer(topk_idx, "topk_idx", _I32S, n, device),
+                                          _buffer(dgate, "dgate", _F32, n, device), to, ldd,
                                           _stream(stream)), "mok_route_scored_backward")
 
 
 def mok_route_bias_update(load, n_layers: int, E: int, rate: float, bias, clear_load: int = 0,
                           stream=None) -> None:
-    _check(_lib.mok_route_bias_update(_buffer(load, "load", (torch.int32,), n_layers * E), n_layers,
-                                      E, rate, _buffer(bias, "bias", (torch.float32,), n_layers * E),
-                                      clear_load, _stream(stream)), "mok_route_bias_update")
+    n, device = n_layers * E, _device()
+    _check(_lib.mok_route_bias_update(_buffer(load, "load", _I32S, n, device), n_layers, E, rate,
+                                      _buffer(bias, "bias", _F32, n, device), clear_load,
+                                      _stream(stream)), "mok_route_bias_update")
 
 
 class AdamwTensors:
@@ -307,20 +315,20 @@ class AdamwTensors:
     def __init__(self, tensors: Sequence[dict], stream=None):
         self.tensors = [dict(t) for t in tensors]
         self.c = (mok_adamw_tensor * len(self.tensors))()
-        f32, u8 = (torch.float32,), (torch.uint8,)
+        device = _device()
         for c, t in zip(self.c, self.tensors):
             n = t["p"].numel()
             coded = t["m"].dtype == torch.uint8
-            for name, kinds, size in (("p", f32, n), ("grad", tuple(_TYPES), n),
-                                      ("m", u8 if coded else f32, n), ("v", u8 if coded else f32, n),
-                                      ("p_bf16", (torch.bfloat16,), n),
-                                      ("m_scale", u8, (n + 31) // 32), ("v_scale", u8, (n + 31) // 32)):
+            state, blocks = _U8 if coded else _F32, (n + 31) // 32
+            for name, kinds, size in (("p", _F32, n), ("grad", tuple(_TYPES), n), ("m", state, n),
+                                      ("v", state, n), ("p_bf16", _BF16, n), ("m_scale", _U8, blocks),
+                                      ("v_scale", _U8, blocks)):
                 x = t.get(name)
                 if x is None and (name == "p_bf16" or (name.endswith("scale") and not coded)):
                     continue
                 if x is None:
                     raise ValueError(f"{name}: missing")
-                address = _buffer(x, name, kinds, size)
+                address = _buffer(x, name, kinds, size, device)
                 if x.numel() != size:
                     raise ValueError(f"{name}: {x.numel()} elements where {size} are wanted")
                 setattr(c, name, address)
@@ -352,9 +360,10 @@ def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float,
     """scalars: None, or 16 bytes on the GPU as a ``mok_adamw_scalars`` (lr and grad_scale fp32,
     step and skip int32)."""
     if scalars is not None and not isinstance(scalars, int):
-        if scalars.numel() * scalars.element_size() != 16 or not scalars.is_contiguous():
+        size = scalars.element_size()
+        if scalars.numel() * size != 16:
             raise ValueError("scalars: 16 dense bytes are wanted")
-        scalars = _on_device(scalars, "scalars")
+        scalars = _buffer(scalars, "scalars", (scalars.dtype,), 16 // size, _device())
     h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
     _check(_lib.mok_adamw_step(_ptr(tensors.table), C.byref(tensors.plan), C.byref(h), scalars or 0,
                                _stream(stream)), "mok_adamw_step")
@@ -520,13 +529,13 @@ def mok_moe_forward_scored(desc: mok_layer_desc, router: mok_router_desc, logits
                            w_gate_up, w_down, out: Tokens, ws, bias=None, topk_idx=None,
                            topk_gate=None, load=None, ws_bytes: Optional[int] = None,
                            stream=None) -> None:
-    E, n = router.n_experts, T * router.top_k
-    at, kind, ld = _rows(logits, "logits", T, E)
+    E, n, device = router.n_experts, T * router.top_k, _device()
+    at, kind, ld = _rows(logits, "logits", T, E, device)
     _check(_lib.mok_moe_forward_scored(C.byref(desc), C.byref(router), at, kind, ld,
-                                       _buffer(bias, "bias", (torch.float32,), E), T,
-                                       _buffer(topk_idx, "topk_idx", (torch.int32,), n),
-                                       _buffer(topk_gate, "topk_gate", (torch.float32,), n),
-                                       _buffer(load, "load", (torch.int32,), E), C.byref(x.c),
+                                       _buffer(bias, "bias", _F32, E, device), T,
+                                       _buffer(topk_idx, "topk_idx", _I32S, n, device),
+                                       _buffer(topk_gate, "topk_gate", _F32, n, device),
+                                       _buffer(load, "load", _I32S, E, device), C.byref(x.c),
                                        _ptr(w_gate_up), _ptr(w_down), C.byref(out.c), _ptr(ws),
                                        _ws_bytes(ws, ws_bytes), _stream(stream)),
            "mok_moe_forward_scored")
