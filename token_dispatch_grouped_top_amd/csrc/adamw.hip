@@ -3,20 +3,35 @@
 //
 // A table in device memory, written once for a program's buffers, holds the
 // tensors' addresses and factors, and the first unit of each: the 1024 elements
-// (2048 with 8-bit states) of one workgroup.  Small units keep what is in flight
-// at any time in one run of memory: 352 M elements with fp32 states take 1.62 ms
-// so, 1.85 ms in units of 8192, and 2.0 ms where 2048 workgroups take the units
-// in turn and drift apart.  A workgroup finds its tensor with one load per lane
-// and a ballot for each power of 64 in the number of tensors, and works out the
-// step's factors while its elements are on their way.  A thread has four
-// consecutive elements, so that every access of a wave is contiguous and the 32
-// elements of an 8-bit block lie in eight lanes.
+// (2048 with 8-bit states) of one workgroup.  A workgroup finds its tensor with
+// one load per lane and a ballot for each power of 64 in the number of tensors,
+// and works out the step's factors while its elements are on their way.  A
+// thread has four consecutive elements, so that every access of a wave is
+// contiguous and the 32 elements of an 8-bit block lie in eight lanes.
 //
-// Bound by HBM: 28 bytes an element with fp32 states, bf16 gradients and copy,
-// 16 1/8 with 8-bit states.
+// Bound by HBM: 28 bytes an element with fp32 states, bf16 gradients and copy:
+// 352 M in 1.53 ms, 6.45 TB/s; 16 1/8 with 8-bit states: 88 M in 0.25 ms, 5.6 TB/s
+// (a large copy moves 5.2).  What counts is how near to each other the runs of
+// memory are that are read and written at a time:
+//   - small units: fp32 states in units of 8192 elements 1.85 ms, and 2.0 where
+//     2048 workgroups take the units in turn and drift apart;
+//   - few waves in flight: fp32 states 1.72 ms with 8 waves a SIMD, 1.60 with 5
+//     or 4, 1.75 with 3; with 8-bit states latency counts more: 0.25 ms with 7
+//     waves, 0.27 with 6, 0.29 with 5;
+//   - 64 units in a row for each XCD: 1.60 -> 1.53 ms (128: 1.61; with 8-bit
+//     states no gain);
+//   - nontemporal loads and stores: 6 and 4 %.
+// With 8-bit states two units of loads are under way at once (0.25 ms; one 0.30,
+// three 0.28), and the vector instructions are near: 80 an element, 0.2 ms.  What
+// is rare (a value that is not finite, r below 2^-50, a code below 2^-6 of the
+// scale) is left to a second path that a whole wave takes.
+// One tensor of 2048 elements 2.6 us (fp32) and 4.4 us, 200 tensors of 4096 to
+// 13000 elements 11 us.
 //
 // The order of the fp32 operations on the states is fixed (no contraction): the
 // 8-bit codes follow from the bits of m and v.
+#include <cmath>
+
 #include "mok_internal.h"
 
 namespace mok {
@@ -26,7 +41,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroup = kThreads * 4;              // elements of a workgroup at a time
 constexpr int kBatch = 40;                        // tensors of one table-writing launch
-constexpr int kF32Waves = 5, kMxWaves = 7;
+constexpr int kF32Waves = 5, kMxWaves = 7;        // a SIMD
+constexpr uint32_t kXcds = 8, kRun = 64;          // units that follow each other on one XCD
 constexpr int kMxGroups = 2;                      // groups of a unit with 8-bit states
 
 struct TensorArg {
@@ -63,8 +79,10 @@ __global__ void k_adamw_table(TableArg a, int64_t* units, TensorArg* t) {
 
 struct StepArg {
   double lr, beta1, beta2;
-  float eps, grad_scale;
-  int32_t step;
+  double per_m;                                   // lr / (1 - beta1^t), and
+  float inv_bc2;                                  // 1 / sqrt(1 - beta2^t), of the host's step
+  uint32_t step_key;
+  float b1, c1, b2, c2, eps, grad_scale;
   uint32_t seed;
   const mok_adamw_scalars* scalars;
   const int64_t* units;
@@ -72,7 +90,7 @@ struct StepArg {
   int32_t n_tensors;
 };
 
-__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+__host__ __device__ __forceinline__ uint32_t hash32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x9E3779B1u;
   x = (x ^ (x >> 15)) * 0xBB67AE85u;
   return x ^ (x >> 16);
@@ -140,8 +158,8 @@ __device__ __forceinline__ uint32_t encode_r_normal(float a, uint32_t b16) {
 #pragma clang fp contract(off)
   const uint32_t u = __float_as_uint(a) & 0xfff00000u;
   const float low = __uint_as_float(u), high = __uint_as_float(u + 0x100000u);
-  const float have = (a - low) * (a + low), span = (high - low) * (high + low);
-  return (u >> 20) - 960u + (have > unit_of(b16) * span ? 1u : 0u);
+  const float have = (a - low) * (a + low), span = fmaf(high, high, -(low * low));   // exact
+  return (u >> 20) + (have > unit_of(b16) * span ? 1u - 960u : 0u - 960u);
 }
 
 struct Factors {
@@ -166,6 +184,9 @@ __device__ __forceinline__ float parameter(const Factors& f, float p, float m, f
   const float d = fmaf(r, f.inv_bc2, f.eps);
   return fmaf(-f.rate, m * __builtin_amdgcn_rcpf(d), p * f.keep);
 }
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
 
 // Largest of the eight lanes that share a block of 32 elements.
 __device__ __forceinline__ float max8(float v) {
@@ -270,11 +291,12 @@ __device__ __forceinline__ void work(const TensorArg& t, const Factors& f, uint3
     states(f, o.g[j], m[j], v[j]);
     if (MX && j >= have) m[j] = v[j] = 0.0f;
   }
-  // the plain way for a wave with a value that is not finite, or v below the range of rsq
-  const float lowest = fminf(fminf(v[0], v[1]), fminf(v[2], v[3]));
-  const float all = (fabsf(m[0]) + fabsf(m[1])) + (fabsf(m[2]) + fabsf(m[3])) +
-                    ((v[0] + v[1]) + (v[2] + v[3]));
-  const bool odd = __ballot(!(lowest >= 0x1p-100f && all < __builtin_inff())) != 0;
+  // the plain way for a wave with a v that is not finite, or below the range of rsq (v is not
+  // negative: its bits are in its order, a NaN's above all)
+  const uint32_t b0 = __float_as_uint(v[0]), b1 = __float_as_uint(v[1]), b2 = __float_as_uint(v[2]),
+                 b3 = __float_as_uint(v[3]);
+  const uint32_t most = umax(umax(umax(b0, b1), b2), b3), lowest = umin(umin(umin(b0, b1), b2), b3);
+  const bool odd = __ballot(most >= 0x7f800000u || lowest < 0x0d800000u) != 0;   // inf; 2^-100
 #pragma unroll
   for (int j = 0; j < 4; ++j) r[j] = odd ? sqrtf(v[j]) : sqrt_normal(v[j]);
 #pragma unroll
@@ -293,11 +315,11 @@ __device__ __forceinline__ void work(const TensorArg& t, const Factors& f, uint3
     }
     const int em = state_scale_exp(max8(am)), er = state_scale_exp(max8(ar));
     uint32_t h[4];
+    // four neighbours never lie on both sides of a multiple of 2^32
+    const uint32_t at = static_cast<uint32_t>(i0) +
+                        static_cast<uint32_t>(static_cast<uint64_t>(i0) >> 32) * 0x6A09E667u + key;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t i = static_cast<uint64_t>(i0) + j;
-      h[j] = hash32(static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x6A09E667u + key);
-    }
+    for (int j = 0; j < 4; ++j) h[j] = hash32(at + j);
     float a[4], b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -306,8 +328,10 @@ __device__ __forceinline__ void work(const TensorArg& t, const Factors& f, uint3
     }
     const float least = fminf(fminf(fminf(a[0], a[1]), fminf(a[2], a[3])),
                               fminf(fminf(b[0], b[1]), fminf(b[2], b[3])));
+    // (a NaN among the m would not show in `least`)
+    const bool plain = !(least >= 0.015625f && (a[0] + a[1]) + (a[2] + a[3]) < 2048.0f);
     mw = vw = 0;
-    if (odd || __ballot(!(least >= 0.015625f))) {
+    if (odd || __ballot(plain)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         mw |= encode_m(m[j], em, h[j] & 0xffffu) << (8 * j);
@@ -375,29 +399,31 @@ __device__ __forceinline__ int tensor_of(const int64_t* __restrict__ units, int 
   return __builtin_amdgcn_readfirstlane(first);
 }
 
-// The step's numbers, from the host or from device memory; false: nothing is done.
+typedef const __attribute__((address_space(4))) mok_adamw_scalars* ScalarsPtr;
+
+// The step's numbers, from the host or from device memory; false: nothing is
+// done.  What depends on the step alone comes from the host where it knows it:
+// in fp64 on the vector units it is 200 instructions of each wave.
 __device__ __forceinline__ bool factors(const StepArg& h, float lr_scale, float weight_decay,
                                         uint32_t number, Factors& f, uint32_t& key) {
-  double lr = h.lr;
+  f.b1 = h.b1; f.c1 = h.c1; f.b2 = h.b2; f.c2 = h.c2; f.eps = h.eps;
+  double lr = h.lr, per_m = h.per_m;
   f.gs = h.grad_scale;
-  int32_t step = h.step;
+  f.inv_bc2 = h.inv_bc2;
+  uint32_t step_key = h.step_key;
   if (h.scalars) {
-    const mok_adamw_scalars sc = *h.scalars;
-    if (sc.skip != 0 || sc.step < 1) return false;
-    lr = sc.lr;
-    f.gs = sc.grad_scale;
-    step = sc.step;
+    const ScalarsPtr sc = (ScalarsPtr)(uintptr_t)h.scalars;
+    const int32_t step = sc->step;
+    if (sc->skip != 0 || step < 1) return false;
+    lr = sc->lr;
+    f.gs = sc->grad_scale;
+    per_m = static_cast<double>(sc->lr / static_cast<float>(1.0 - power(h.beta1, step)));
+    f.inv_bc2 = 1.0f / sqrtf(static_cast<float>(1.0 - power(h.beta2, step)));
+    step_key = hash32(h.seed + 0x9E3779B1u * static_cast<uint32_t>(step));
   }
-  f.b1 = static_cast<float>(h.beta1);
-  f.c1 = static_cast<float>(1.0 - h.beta1);
-  f.b2 = static_cast<float>(h.beta2);
-  f.c2 = static_cast<float>(1.0 - h.beta2);
-  lr *= static_cast<double>(lr_scale);
-  f.keep = static_cast<float>(1.0 - lr * static_cast<double>(weight_decay));
-  f.rate = static_cast<float>(lr / (1.0 - power(h.beta1, step)));
-  f.inv_bc2 = static_cast<float>(1.0 / sqrt(1.0 - power(h.beta2, step)));
-  f.eps = h.eps;
-  key = hash32(hash32(h.seed + 0x9E3779B1u * static_cast<uint32_t>(step)) + number);
+  f.keep = static_cast<float>(1.0 - lr * static_cast<double>(lr_scale) * static_cast<double>(weight_decay));
+  f.rate = static_cast<float>(per_m * static_cast<double>(lr_scale));
+  key = hash32(step_key + number);
   return true;
 }
 
@@ -423,7 +449,11 @@ __device__ __forceinline__ void unit(const TensorArg& t, const StepArg& h, int64
 template <bool MX>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, MX ? kMxWaves : kF32Waves)))
 void k_adamw(StepArg h) {
-  const int64_t u = blockIdx.x;
+  int64_t u = blockIdx.x;
+  if (!MX) {                                            // workgroups go round the XCDs: runs of units for each
+    const uint32_t run = kXcds * kRun, block = blockIdx.x / run, in = blockIdx.x % run;
+    if (block < gridDim.x / run) u = static_cast<int64_t>(block) * run + in % kXcds * kRun + in / kXcds;
+  }
   const TablePtr p = (TablePtr)(uintptr_t)(h.tensors + tensor_of(h.units, h.n_tensors, u));
   TensorArg t;
   t.p = p->p; t.pb = p->pb; t.g = p->g; t.m = p->m; t.v = p->v; t.ms = p->ms; t.vs = p->vs;
@@ -479,8 +509,22 @@ hipError_t launch_adamw(const void* table, const mok_adamw_plan& plan, const mok
                         const mok_adamw_scalars* scalars, hipStream_t s) {
   const int64_t* units = static_cast<const int64_t*>(table);
   const TensorArg* t = reinterpret_cast<const TensorArg*>(static_cast<const uint8_t*>(table) + descriptors_at(plan.list));
-  StepArg a{h.lr, h.beta1, h.beta2, static_cast<float>(h.eps), static_cast<float>(h.grad_scale),
-            h.step, h.seed, scalars, units, t, plan.n_tensors[0]};
+  StepArg a{};
+  a.lr = h.lr; a.beta1 = h.beta1; a.beta2 = h.beta2;
+  a.b1 = static_cast<float>(h.beta1); a.c1 = static_cast<float>(1.0 - h.beta1);
+  a.b2 = static_cast<float>(h.beta2); a.c2 = static_cast<float>(1.0 - h.beta2);
+  a.eps = static_cast<float>(h.eps);
+  a.seed = h.seed;
+  a.scalars = scalars;
+  if (!scalars) {
+    a.grad_scale = static_cast<float>(h.grad_scale);
+    a.per_m = h.lr / (1.0 - std::pow(h.beta1, h.step));
+    a.inv_bc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(h.beta2, h.step)));
+    a.step_key = hash32(h.seed + 0x9E3779B1u * static_cast<uint32_t>(h.step));
+  }
+  a.units = units;
+  a.tensors = t;
+  a.n_tensors = plan.n_tensors[0];
   if (plan.n_units[0] > 0) {
     hipLaunchKernelGGL(k_adamw<false>, dim3(static_cast<uint32_t>(plan.n_units[0])), dim3(kThreads), 0, s, a);
     const hipError_t e = hipGetLastError();

@@ -18,8 +18,16 @@
 // than their error, the groups' values are formed in fp64 (exact_groups).
 // Where more candidates are left than lanes (many equal logits), the wave takes
 // the plain way (exact_picks): fp64 for every expert and k rounds of argmax.
-// Keys are kept as integers in the floats' order: their reductions over lanes
-// are one DPP instruction a level.
+// Reductions over lanes are of integers in the floats' order: one DPP
+// instruction a level.
+//
+// Bound by the issue of vector instructions, not by HBM: 780 a wave of four
+// tokens over 256 experts (a key takes 15, the rest is the same for any number).
+// 16384 tokens in 8 groups 8.8 us, 65536 23.8 us (their logits alone take 3.2 and
+// 13 us at the rate of a large copy); 384 experts without groups 9.5 and 28.8 us.
+// One token 4.1 us, half of it the launch.  (A first version with an fp64 score
+// of every logit, k rounds of argmax over 64 lanes and an atomic for each pick
+// took 174 us for the 16384 tokens with their load; now 11.5.)
 //
 // Lanes.  A token has kL = 16 or 64 lanes.  Every group of experts gets m
 // neighbouring lanes (the largest power of two with m G <= kL), each a run of
@@ -51,7 +59,8 @@ constexpr float kLog2e = 1.44269504f;
 // experts in bf16: 4096 tokens 3.5 and 3.35 us, 16384 4.8 and 7.0), dense
 // backward (16384 10.3 and 9.4 us, 65536 29.0 and 27.6; 160 experts 21.7 and 25.8).
 constexpr int kManyTokens = 2048, kManySparse = 8192, kManyDense = 32768;
-// Picks up to which each adds to the load by itself.
+// Picks up to which each adds to the load by itself: about 1 ns a pick on the
+// same few lines, against a second launch of 2.2 to 3 us.
 constexpr int kDirectPicks = 2048;
 
 template <bool BF16>
@@ -603,8 +612,8 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
 }
 
 // The load of many picks: a workgroup counts its share in LDS and adds each
-// expert's count once.  (One atomic for each pick costs about 1 ns, all of them
-// on the same few lines: 131072 picks of 256 experts 130 us.)
+// expert's count once: 131072 picks of 256 experts in 2.6 us (one atomic a pick:
+// 130 us).
 constexpr int kLoadThreads = 1024, kLoadPicks = 4 * kLoadThreads;
 
 __global__ __launch_bounds__(kLoadThreads)
@@ -635,7 +644,11 @@ void k_load_count(const int32_t* __restrict__ idx, int64_t n, int32_t E, int32_t
 // (softmax without renorm): with the picks' weights w in the row,
 //   D = sum_e s_e w_e,  dl_e = s_e (w_e - D),
 // the logits in registers, V of them to a lane, four neighbours at a time.
-// Bound by the row's write (and for the dense form its read).
+// Bound by the row's write (and for the dense form its read): 16384 tokens over
+// 256 experts sparse 6.1 us in fp32, 4.8 in bf16, dense 9.4 and 8.6; 65536 sparse
+// 18.1 us (3.7 TB/s).  Zeros written before the picks' values instead of a row in
+// LDS: 3.6 us where this takes 3.7 at 4096 tokens, 19.7 where it takes 18.1 at
+// 65536.
 template <int kL, int V, bool BF16>
 __global__ __launch_bounds__(kWaves * kWave)
 void k_route_scored_bwd(RouterArgs r, const void* __restrict__ logits, int64_t ld, int32_t T,
@@ -795,8 +808,8 @@ void k_route_scored_bwd(RouterArgs r, const void* __restrict__ logits, int64_t l
 }
 
 // The bias update: one workgroup per layer, an expert to a thread as far as
-// 1024 threads go.  The load's sum in 64-bit integers, then the bias.  Launch
-// latency: 2 us for any size up to 1024 experts.
+// 1024 threads go.  The load's sum in 64-bit integers, then the bias.  Bound by
+// latency: 1.9 us for one layer of 384 experts, 3.5 us for 60 of 1000.
 constexpr int kBiasThreads = 1024;
 
 __global__ __launch_bounds__(kBiasThreads)
