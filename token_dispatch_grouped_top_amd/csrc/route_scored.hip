@@ -3,10 +3,10 @@
 // the bias.
 //
 // The order of two experts is that of their choice values c = s + bias in
-// fp64, because fp32 does not tell them apart often enough (of 16384 tokens
-// over 256 experts about ten have two neighbours in their order within fp32's
-// error).  An fp64 exponential of every logit costs more than all the rest,
-// so a token's experts go through two steps:
+// fp64, because fp32 does not always tell them apart (about one batch of 16384
+// tokens over 256 experts in four has a token that fp32 picks for differently).
+// An fp64 exponential of every logit costs more than all the rest, so a token's
+// experts go through two steps:
 //   1. fp32 keys (c with a known error; without a bias the logits
 //      themselves, whose order is the scores') find a value t0 that at least k
 //      experts reach, and the candidates are those with a key of at least
