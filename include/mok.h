@@ -736,7 +736,8 @@ mok_status mok_moe_forward_router(const mok_layer_desc* desc, const void* w_rout
  * and top_k equal to desc's; logits, logits_type, ld, bias and load as there):
  * the scored route also counts the local picks for the schedule, then the
  * steps of mok_moe_forward.  Results are those of mok_route_scored followed by
- * mok_moe_forward_routed, bit for bit.  topk_idx / topk_gate: the routing is
+ * mok_moe_forward_routed, bit for bit.  ws: mok_forward_workspace_size(desc,
+ * T, 1) bytes.  topk_idx / topk_gate: the routing is
  * written there (int32 / fp32 [T][k], what the backward reads), or into the
  * workspace if both are NULL. */
 mok_status mok_moe_forward_scored(const mok_layer_desc* desc, const mok_router_desc* router,

@@ -350,12 +350,13 @@ def test_route_on_a_side_stream_and_replayed_from_a_graph():
         assert np.array_equal(bias.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("T", [300, 2100])
 @pytest.mark.parametrize("mode", [0, 1])
 @pytest.mark.parametrize("base,n_local", [(0, 16), (5, 8)])
-def test_fused_layer_with_the_scored_route(mode, base, n_local):
+def test_fused_layer_with_the_scored_route(mode, base, n_local, T):
     """mok_moe_forward_scored is mok_route_scored followed by mok_moe_forward_routed, bit for bit, with rows that
     pick fewer than k experts or none."""
-    wl = W.logits_workload("scored", 31, T=300, H=256, I=128, E=16, k=4, x_std=1.0, w_std=0.02, expert_base=base,
+    wl = W.logits_workload("scored", 31, T=T, H=256, I=128, E=16, k=4, x_std=1.0, w_std=0.02, expert_base=base,
                            n_local=n_local, n_partitions=3)
     dw = DeviceWorkload(wl)
     logits = dw.logits.clone()
@@ -363,20 +364,20 @@ def test_fused_layer_with_the_scored_route(mode, base, n_local):
     logits[50:60] = float("nan")
     bias = 0.1 * torch.randn(16, device="cuda")
     r = _router(16, 4, ref.SIGMOID, 4, 2, True, True, 2.5)
-    idx = torch.empty(300, 4, dtype=torch.int32, device="cuda")
-    gate = torch.empty(300, 4, device="cuda")
+    idx = torch.empty(T, 4, dtype=torch.int32, device="cuda")
+    gate = torch.empty(T, 4, device="cuda")
     load = torch.zeros(16, dtype=torch.int32, device="cuda")
-    mok.mok_route_scored(r, logits, 300, idx, gate, bias=bias, load=load)
+    mok.mok_route_scored(r, logits, T, idx, gate, bias=bias, load=load)
     d = dw.desc(mode=mode)
-    ws = torch.empty(mok.mok_forward_workspace_size(d, 300, 1), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(mok.mok_forward_workspace_size(d, T, 1), dtype=torch.uint8, device="cuda")
     want, got, inside = dw.outs[0], dw.new_out(), dw.new_out()
-    mok.mok_moe_forward_routed(d, idx, gate, 300, dw.x, dw.w_gu, dw.w_d, want, ws)
+    mok.mok_moe_forward_routed(d, idx, gate, T, dw.x, dw.w_gu, dw.w_d, want, ws)
     assert mok.mok_device_status(ws) == 0
     idx2, gate2, load2 = torch.empty_like(idx), torch.empty_like(gate), torch.zeros_like(load)
-    mok.mok_moe_forward_scored(d, r, logits, 300, dw.x, dw.w_gu, dw.w_d, got, ws, bias=bias, topk_idx=idx2,
+    mok.mok_moe_forward_scored(d, r, logits, T, dw.x, dw.w_gu, dw.w_d, got, ws, bias=bias, topk_idx=idx2,
                                topk_gate=gate2, load=load2)
     assert mok.mok_device_status(ws) == 0
-    mok.mok_moe_forward_scored(d, r, logits, 300, dw.x, dw.w_gu, dw.w_d, inside, ws, bias=bias)
+    mok.mok_moe_forward_scored(d, r, logits, T, dw.x, dw.w_gu, dw.w_d, inside, ws, bias=bias)
     assert mok.mok_device_status(ws) == 0
     assert torch.equal(idx, idx2) and torch.equal(gate, gate2) and torch.equal(load, load2)
     rows = dw.out_rows(want)
