@@ -234,19 +234,28 @@ def _device() -> int:
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
 
 
+def _stream_of(stream, device: int) -> int:
+    """_stream with the current GPU at hand."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None and device >= 0 else _stream(stream)
+
+
+# The checks of a call are a part of its latency: what is right passes on one line, the error is
+# worked out behind it.
 def _buffer(x, name: str, dtypes, n: int, device: int) -> int:
     """Address of a buffer of at least n elements: None, a raw address (not checked), or a dense
     tensor of one of dtypes on the GPU `device`."""
-    if x is None or isinstance(x, int):
-        return x or 0
+    if x is None:
+        return 0
+    if type(x) is int:
+        return x
+    if x.dtype in dtypes and x.is_contiguous() and x.numel() >= n and x.get_device() == device >= 0:
+        return x.data_ptr()
     if x.dtype not in dtypes:
         raise ValueError(f"{name}: {x.dtype} where {' or '.join(map(str, dtypes))} is wanted")
     if not x.is_contiguous() or x.numel() < n:
         raise ValueError(f"{name}: {tuple(x.shape)} with strides {x.stride()} where {n} dense elements "
                          "are wanted")
-    if x.get_device() != device or device < 0:
-        raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
-    return x.data_ptr()
+    raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
 
 
 def _rows(x, name: str, T: int, E: int, device: int):
@@ -256,13 +265,14 @@ def _rows(x, name: str, T: int, E: int, device: int):
     kind = _TYPES.get(x.dtype)
     if kind is None:
         raise ValueError(f"{name}: {x.dtype} where torch.float32 or torch.bfloat16 is wanted")
-    shape, (ld, step) = x.shape, x.stride() if x.dim() == 2 else (0, 0)
-    if ld == 0 and step == 0 or shape[0] < T or shape[1] != E or (E > 1 and step != 1):
-        raise ValueError(f"{name}: {tuple(shape)} with strides {x.stride()} where [{T}][{E}] rows of "
-                         "dense values are wanted")
-    if x.get_device() != device or device < 0:
-        raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
-    return x.data_ptr(), kind, ld if T > 1 else max(ld, E)
+    if x.dim() == 2:
+        (rows, width), (ld, step) = x.shape, x.stride()
+        if rows >= T and width == E and (step == 1 or E == 1) and x.get_device() == device >= 0:
+            return x.data_ptr(), kind, ld if T > 1 else max(ld, E)
+        if rows >= T and width == E and (step == 1 or E == 1):
+            raise ValueError(f"{name}: on {x.device}, which is not the current GPU")
+    raise ValueError(f"{name}: {tuple(x.shape)} with strides {x.stride()} where [{T}][{E}] rows of "
+                     "dense values are wanted")
 
 
 _F32, _I32S, _U8, _BF16 = (torch.float32,), (torch.int32,), (torch.uint8,), (torch.bfloat16,)
@@ -276,7 +286,7 @@ def mok_route_scored(router: mok_router_desc, logits, T: int, topk_idx, topk_gat
                                  _buffer(bias, "bias", _F32, E, device), T,
                                  _buffer(topk_idx, "topk_idx", _I32S, n, device),
                                  _buffer(topk_gate, "topk_gate", _F32, n, device),
-                                 _buffer(load, "load", _I32S, E, device), _stream(stream)),
+                                 _buffer(load, "load", _I32S, E, device), _stream_of(stream, device)),
            "mok_route_scored")
 
 
@@ -290,7 +300,7 @@ def mok_route_scored_backward(router: mok_router_desc, logits, T: int, topk_idx,
     _check(_lib.mok_route_scored_backward(C.byref(router), at, kind, ld, T,
                                           _buffer(topk_idx, "topk_idx", _I32S, n, device),
                                           _buffer(dgate, "dgate", _F32, n, device), to, ldd,
-                                          _stream(stream)), "mok_route_scored_backward")
+                                          _stream_of(stream, device)), "mok_route_scored_backward")
 
 
 def mok_route_bias_update(load, n_layers: int, E: int, rate: float, bias, clear_load: int = 0,
@@ -298,7 +308,7 @@ def mok_route_bias_update(load, n_layers: int, E: int, rate: float, bias, clear_
     n, device = n_layers * E, _device()
     _check(_lib.mok_route_bias_update(_buffer(load, "load", _I32S, n, device), n_layers, E, rate,
                                       _buffer(bias, "bias", _F32, n, device), clear_load,
-                                      _stream(stream)), "mok_route_bias_update")
+                                      _stream_of(stream, device)), "mok_route_bias_update")
 
 
 class AdamwTensors:
@@ -309,7 +319,8 @@ class AdamwTensors:
     codes beside ``m_scale`` and ``v_scale``, uint8), and optionally ``p_bf16``, ``lr_scale`` (1)
     and ``weight_decay`` (0).  Dense tensors of the same number of elements on one GPU.  Built
     once for a program's buffers, on the stream given (waited for, unless it is being captured:
-    the list can then be used on any stream).
+    the list can then be used on any stream).  A program that lets torch allocate new gradients
+    for a step builds a new list for them.
     """
 
     def __init__(self, tensors: Sequence[dict], stream=None):
@@ -335,10 +346,11 @@ class AdamwTensors:
             c.n, c.grad_type = n, _TYPES[t["grad"].dtype]
             c.state_format = MOK_STATE_MXFP8 if coded else MOK_STATE_F32
             c.lr_scale, c.weight_decay = t.get("lr_scale", 1.0), t.get("weight_decay", 0.0)
-        self.plan, self.table = mok_adamw_plan(), None
+        self.plan, self.table, self.address = mok_adamw_plan(), None, 0
         if self.tensors:
             size = mok_adamw_table_size(len(self.c))
             self.table = torch.empty(size, dtype=torch.uint8, device=self.tensors[0]["p"].device)
+            self.address = self.table.data_ptr()
             mok_adamw_build_table(self.c, self.table, self.plan, stream)
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.synchronize()
@@ -365,8 +377,8 @@ def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float,
             raise ValueError("scalars: 16 dense bytes are wanted")
         scalars = _buffer(scalars, "scalars", (scalars.dtype,), 16 // size, _device())
     h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
-    _check(_lib.mok_adamw_step(_ptr(tensors.table), C.byref(tensors.plan), C.byref(h), scalars or 0,
-                               _stream(stream)), "mok_adamw_step")
+    _check(_lib.mok_adamw_step(tensors.address, C.byref(tensors.plan), C.byref(h), scalars or 0,
+                               _stream_of(stream, _device())), "mok_adamw_step")
 
 
 def mok_route_gemm_workspace_size(T: int, E: int, H: int) -> int:
@@ -537,7 +549,7 @@ def mok_moe_forward_scored(desc: mok_layer_desc, router: mok_router_desc, logits
                                        _buffer(topk_gate, "topk_gate", _F32, n, device),
                                        _buffer(load, "load", _I32S, E, device), C.byref(x.c),
                                        _ptr(w_gate_up), _ptr(w_down), C.byref(out.c), _ptr(ws),
-                                       _ws_bytes(ws, ws_bytes), _stream(stream)),
+                                       _ws_bytes(ws, ws_bytes), _stream_of(stream, device)),
            "mok_moe_forward_scored")
 
 
