@@ -1,0 +1,114 @@
+"""Host checks of the AdamW list's own device table: which stream's memory it
+is, on which stream it is written, and what is waited for.  torch's streams are
+stood in for, so that the order of the calls can be looked at without a GPU."""
+import contextlib
+
+import pytest
+import torch
+
+import token_dispatch_grouped_top_amd as mok
+
+
+class Stream:
+    def __init__(self, handle, gpu=0):
+        self.cuda_stream, self.device, self.capturing = handle, torch.device("cuda", gpu), False
+
+
+class Buffer:
+    """A dense tensor on the stand-in's GPU 0, taken from the current stream's memory."""
+
+    def __init__(self, gpu, n, dtype=torch.float32):
+        self.gpu, self.n, self.dtype, self.home = gpu, n, dtype, gpu.current
+        self.device, self.shape, self.used_on = torch.device("cuda", 0), (n,), []
+
+    def numel(self):
+        return self.n
+
+    def stride(self):
+        return (1,)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def record_stream(self, stream):
+        self.gpu.log.append(("record", self, stream.cuda_stream))
+        self.used_on.append(stream.cuda_stream)
+
+
+class Gpu:
+    def __init__(self):
+        self.default = self.current = Stream(0)
+        self.log, self.device = [], 0
+
+    def tensors(self, count=2):
+        return [{name: Buffer(self, 64) for name in ("p", "grad", "m", "v")} for _ in range(count)]
+
+    def did(self, what):
+        return [x[1:] for x in self.log if x[0] == what]
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    g = Gpu()
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, g.current = g.current, stream
+        yield
+        g.current = before
+
+    def wait(name):
+        return lambda self=None, *a: g.log.append((name, self or g.current))
+
+    def external(handle, device=None):
+        assert handle != 0                     # torch makes a new stream of a handle of 0
+        return Stream(handle)
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: g.current)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: g.default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: g.current.capturing)
+    monkeypatch.setattr(torch.cuda, "synchronize", wait("synchronize all"))
+    monkeypatch.setattr(Stream, "synchronize", wait("synchronize"), raising=False)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype=None, device=None: Buffer(g, n, dtype))
+    monkeypatch.setattr(mok, "_device", lambda: g.device)
+    monkeypatch.setattr(mok, "_stream_of",
+                        lambda s, device: g.current.cuda_stream if s is None else s if isinstance(s, int) else s.cuda_stream)
+    monkeypatch.setattr(mok, "_stream", lambda s: mok._stream_of(s, 0))
+    monkeypatch.setattr(mok, "mok_adamw_build_table",
+                        lambda c, table, plan, stream=None: g.log.append(("write", table, mok._stream_of(stream, 0))))
+    return g
+
+
+def _given(g, how):
+    """(the argument, the stream it means)"""
+    side = Stream(7)
+    return {"none": (None, g.current), "object": (side, side), "handle": (9, Stream(9)), "zero": (0, g.default)}[how]
+
+
+@pytest.mark.parametrize("how", ["none", "object", "handle", "zero"])
+@pytest.mark.parametrize("current", [0, 5])
+def test_table_is_memory_of_the_stream_that_writes_it(gpu, how, current):
+    """Else work still pending on the current stream, in whose memory the block was before, could write over it."""
+    gpu.current = gpu.default if current == 0 else Stream(current)
+    argument, stream = _given(gpu, how)
+    before = gpu.current
+    lst = mok.AdamwTensors(gpu.tensors(), stream=argument)
+    (table, written_on), = gpu.did("write")
+    assert table is lst.table
+    assert table.home.cuda_stream == written_on == stream.cuda_stream
+    # that stream alone is waited for, behind the writing
+    (waited,), = gpu.did("synchronize")
+    assert waited.cuda_stream == stream.cuda_stream and not gpu.did("synchronize all")
+    assert [x[0] for x in gpu.log if x[0] != "record"] == ["write", "synchronize"]
+    assert gpu.current is before

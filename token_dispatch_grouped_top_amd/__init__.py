@@ -239,6 +239,15 @@ def _stream_of(stream, device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device) if stream is None and device >= 0 else _stream(stream)
 
 
+def _stream_object(stream):
+    """torch's object of a call's stream argument."""
+    if stream is None:
+        return torch.cuda.current_stream()
+    if isinstance(stream, int):                # ExternalStream(0) would be a new stream
+        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return stream
+
+
 # The checks of a call are a part of its latency: what is right passes on one line, the error is
 # worked out behind it.
 def _buffer(x, name: str, dtypes, n: int, device: int) -> int:
@@ -349,11 +358,14 @@ class AdamwTensors:
         self.plan, self.table, self.address = mok_adamw_plan(), None, 0
         if self.tensors:
             size = mok_adamw_table_size(len(self.c))
-            self.table = torch.empty(size, dtype=torch.uint8, device=self.tensors[0]["p"].device)
-            self.address = self.table.data_ptr()
-            mok_adamw_build_table(self.c, self.table, self.plan, stream)
-            if not torch.cuda.is_current_stream_capturing():
-                torch.cuda.synchronize()
+            on = _stream_object(stream)
+            # memory of the stream that writes it: a block of another stream's may still have work pending there
+            with torch.cuda.stream(on):
+                self.table = torch.empty(size, dtype=torch.uint8, device=self.tensors[0]["p"].device)
+                self.address = self.table.data_ptr()
+                mok_adamw_build_table(self.c, self.table, self.plan, on.cuda_stream)
+                if not torch.cuda.is_current_stream_capturing():
+                    on.synchronize()
 
 
 def mok_adamw_table_size(n_tensors: int) -> int:
