@@ -1,7 +1,9 @@
 """Host checks of the AdamW list's own device table: which stream's memory it
-is, on which stream it is written, and what is waited for.  torch's streams are
-stood in for, so that the order of the calls can be looked at without a GPU."""
+is, on which stream it is written, what is waited for, and which streams' work
+keeps the memory.  torch's streams are stood in for, so that the order of the
+calls can be looked at without a GPU."""
 import contextlib
+import types
 
 import pytest
 import torch
@@ -73,6 +75,7 @@ def gpu(monkeypatch):
         assert handle != 0                     # torch makes a new stream of a handle of 0
         return Stream(handle)
 
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: g.current)
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: g.default)
@@ -87,7 +90,14 @@ def gpu(monkeypatch):
     monkeypatch.setattr(mok, "_stream", lambda s: mok._stream_of(s, 0))
     monkeypatch.setattr(mok, "mok_adamw_build_table",
                         lambda c, table, plan, stream=None: g.log.append(("write", table, mok._stream_of(stream, 0))))
+    monkeypatch.setattr(mok, "_lib", types.SimpleNamespace(
+        mok_adamw_table_size=mok._lib.mok_adamw_table_size,
+        mok_adamw_step=lambda table, plan, hyper, scalars, stream: g.log.append(("step", stream)) or mok.MOK_OK))
     return g
+
+
+def _step(lst, stream=None):
+    mok.mok_adamw_step(lst, 1e-3, 0.9, 0.95, 1e-8, 1, stream=stream)
 
 
 def _given(g, how):
@@ -112,3 +122,45 @@ def test_table_is_memory_of_the_stream_that_writes_it(gpu, how, current):
     assert waited.cuda_stream == stream.cuda_stream and not gpu.did("synchronize all")
     assert [x[0] for x in gpu.log if x[0] != "record"] == ["write", "synchronize"]
     assert gpu.current is before
+
+
+def test_memory_is_kept_for_steps_on_other_streams(gpu):
+    """A list that is dropped while a step runs on a side stream: its table's memory and its tensors' are not given out
+    again before that step is done."""
+    ts = gpu.tensors(3)
+    lst = mok.AdamwTensors(ts)
+    _step(lst)
+    assert not gpu.did("record") or all(s == 0 for _, s in gpu.did("record"))   # nothing to do on their own stream
+    for argument, handle in ((Stream(7), 7), (9, 9), (Stream(7), 7), (9, 9)):
+        gpu.log.clear()
+        first = handle not in lst.table.used_on
+        _step(lst, argument)
+        assert [x for x in gpu.log if x[0] == "step"] == [("step", handle)]
+        assert lst.table.used_on.count(handle) == 1                         # once for each stream is enough
+        assert bool(gpu.did("record")) == first
+        for t in ts:
+            assert all(x.used_on.count(handle) == 1 for x in t.values())
+    gpu.current = Stream(11)                                                # the current stream, another than at the building
+    _step(lst)
+    assert 11 in lst.table.used_on and all(11 in x.used_on for t in ts for x in t.values())
+    gpu.current = gpu.default
+    _step(lst, 0)
+    assert gpu.did("step")[-1] == (0,)
+
+
+def test_table_of_a_side_stream_is_kept_for_steps_on_the_current_one(gpu):
+    lst = mok.AdamwTensors(gpu.tensors(), stream=Stream(7))
+    _step(lst)
+    assert lst.table.home.cuda_stream == 7 and 0 in lst.table.used_on
+    _step(lst, Stream(7))
+    assert all(7 in x.used_on for t in lst.tensors for x in t.values())     # theirs is the current stream's memory
+
+
+def test_an_empty_list_has_nothing_to_keep(gpu):
+    lst = mok.AdamwTensors([])
+    _step(lst, Stream(7))
+    assert gpu.did("step") == [(7,)] and not gpu.did("record")
+
+
+def test_an_empty_list_needs_no_gpu():
+    mok.mok_adamw_step(mok.AdamwTensors([]), 1e-3, 0.9, 0.95, 1e-8, 1, stream=0)

@@ -243,9 +243,10 @@ def _stream_object(stream):
     """torch's object of a call's stream argument."""
     if stream is None:
         return torch.cuda.current_stream()
-    if isinstance(stream, int):                # ExternalStream(0) would be a new stream
-        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return stream
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)                   # ExternalStream(0) would be a new stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
 # The checks of a call are a part of its latency: what is right passes on one line, the error is
@@ -330,6 +331,10 @@ class AdamwTensors:
     once for a program's buffers, on the stream given (waited for, unless it is being captured:
     the list can then be used on any stream).  A program that lets torch allocate new gradients
     for a step builds a new list for them.
+
+    A list may be dropped while a step of it runs, on any stream (a stream given as a raw handle
+    lives as long as the list).  The tensors themselves are those of the current stream, as for
+    torch's operations.  A captured graph holds addresses: keep its lists as long as the graph.
     """
 
     def __init__(self, tensors: Sequence[dict], stream=None):
@@ -355,7 +360,7 @@ class AdamwTensors:
             c.n, c.grad_type = n, _TYPES[t["grad"].dtype]
             c.state_format = MOK_STATE_MXFP8 if coded else MOK_STATE_F32
             c.lr_scale, c.weight_decay = t.get("lr_scale", 1.0), t.get("weight_decay", 0.0)
-        self.plan, self.table, self.address = mok_adamw_plan(), None, 0
+        self.plan, self.table, self.address, self.streams = mok_adamw_plan(), None, 0, set()
         if self.tensors:
             size = mok_adamw_table_size(len(self.c))
             on = _stream_object(stream)
@@ -366,6 +371,20 @@ class AdamwTensors:
                 mok_adamw_build_table(self.c, self.table, self.plan, on.cuda_stream)
                 if not torch.cuda.is_current_stream_capturing():
                     on.synchronize()
+            here = torch.cuda.current_stream()
+            self.table.record_stream(here)
+            self.streams.add(here.cuda_stream)
+
+    def record_stream(self, stream) -> None:
+        """torch's ``Tensor.record_stream`` for the table and the list's tensors: their memory is not
+        given out again before the work that ``stream`` has when they are dropped is done."""
+        if self.table is None:                    # an empty list
+            return
+        on = _stream_object(stream)
+        for x in (self.table, *(x for t in self.tensors for x in t.values())):
+            if hasattr(x, "record_stream"):
+                x.record_stream(on)
+        self.streams.add(on.cuda_stream)
 
 
 def mok_adamw_table_size(n_tensors: int) -> int:
@@ -389,8 +408,11 @@ def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float,
             raise ValueError("scalars: 16 dense bytes are wanted")
         scalars = _buffer(scalars, "scalars", (scalars.dtype,), 16 // size, _device())
     h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
-    _check(_lib.mok_adamw_step(tensors.address, C.byref(tensors.plan), C.byref(h), scalars or 0,
-                               _stream_of(stream, _device())), "mok_adamw_step")
+    on = _stream_of(stream, _device())
+    if on not in tensors.streams:                 # once for each stream but the one that the list was built under
+        tensors.record_stream(stream)
+    _check(_lib.mok_adamw_step(tensors.address, C.byref(tensors.plan), C.byref(h), scalars or 0, on),
+           "mok_adamw_step")
 
 
 def mok_route_gemm_workspace_size(T: int, E: int, H: int) -> int:
