@@ -65,8 +65,10 @@ def gpu(monkeypatch):
     @contextlib.contextmanager
     def on(stream):
         before, g.current = g.current, stream
-        yield
-        g.current = before
+        try:
+            yield
+        finally:
+            g.current = before
 
     def wait(name):
         return lambda self=None, *a: g.log.append((name, self or g.current))
@@ -154,6 +156,28 @@ def test_table_of_a_side_stream_is_kept_for_steps_on_the_current_one(gpu):
     assert lst.table.home.cuda_stream == 7 and 0 in lst.table.used_on
     _step(lst, Stream(7))
     assert all(7 in x.used_on for t in lst.tensors for x in t.values())     # theirs is the current stream's memory
+
+
+def test_a_stream_that_is_captured_is_not_waited_for(gpu):
+    """Neither is the GPU: what counts is the stream that is written on, not the current one."""
+    side = Stream(7)
+    side.capturing = True
+    mok.AdamwTensors(gpu.tensors(), stream=side)
+    assert gpu.did("write") and not gpu.did("synchronize") and not gpu.did("synchronize all")
+    gpu.log.clear()
+    gpu.current = side
+    mok.AdamwTensors(gpu.tensors())
+    assert gpu.did("write") and not gpu.did("synchronize") and not gpu.did("synchronize all")
+
+
+def test_writing_beside_a_capture_is_refused(gpu):
+    """Waiting for another stream would end the current stream's capture; not waiting would leave the captured steps
+    without a table."""
+    gpu.current = Stream(5)
+    gpu.current.capturing = True
+    with pytest.raises(ValueError, match="stream.*captur"):
+        mok.AdamwTensors(gpu.tensors(), stream=Stream(7))
+    assert not gpu.log and gpu.current.cuda_stream == 5
 
 
 def test_an_empty_list_has_nothing_to_keep(gpu):

@@ -328,8 +328,9 @@ class AdamwTensors:
     One dict per tensor: ``p`` (fp32), ``grad`` (fp32 or bf16), ``m`` and ``v`` (fp32, or uint8
     codes beside ``m_scale`` and ``v_scale``, uint8), and optionally ``p_bf16``, ``lr_scale`` (1)
     and ``weight_decay`` (0).  Dense tensors of the same number of elements on one GPU.  Built
-    once for a program's buffers, on the stream given (waited for, unless it is being captured:
-    the list can then be used on any stream).  A program that lets torch allocate new gradients
+    once for a program's buffers, on the stream given, which is waited for: the list can then be
+    used on any stream.  Built during a capture, on a captured stream, it serves the steps of that
+    graph, which writes the table anew on each replay.  A program that lets torch allocate new gradients
     for a step builds a new list for them.
 
     A list may be dropped while a step of it runs, on any stream (a stream given as a raw handle
@@ -363,9 +364,11 @@ class AdamwTensors:
         self.plan, self.table, self.address, self.streams = mok_adamw_plan(), None, 0, set()
         if self.tensors:
             size = mok_adamw_table_size(len(self.c))
-            on = _stream_object(stream)
+            on, captured = _stream_object(stream), torch.cuda.is_current_stream_capturing()
             # memory of the stream that writes it: a block of another stream's may still have work pending there
             with torch.cuda.stream(on):
+                if captured and not torch.cuda.is_current_stream_capturing():
+                    raise ValueError("stream: not captured, while the current stream is")
                 self.table = torch.empty(size, dtype=torch.uint8, device=self.tensors[0]["p"].device)
                 self.address = self.table.data_ptr()
                 mok_adamw_build_table(self.c, self.table, self.plan, on.cuda_stream)
