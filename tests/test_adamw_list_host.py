@@ -180,6 +180,23 @@ def test_writing_beside_a_capture_is_refused(gpu):
     assert not gpu.log and gpu.current.cuda_stream == 5
 
 
+def test_step_of_a_list_on_another_gpu_is_refused(gpu):
+    lst = mok.AdamwTensors(gpu.tensors())
+    gpu.device = 1
+    with pytest.raises(ValueError, match="list.*current GPU"):
+        _step(lst)
+    assert not gpu.did("step")
+    gpu.device = 0
+    _step(lst)
+    assert gpu.did("step") == [(0,)]
+
+
+def test_building_on_a_stream_of_another_gpu_is_refused(gpu):
+    with pytest.raises(ValueError, match="stream.*current GPU"):
+        mok.AdamwTensors(gpu.tensors(), stream=Stream(7, gpu=1))
+    assert not gpu.log
+
+
 def test_an_empty_list_has_nothing_to_keep(gpu):
     lst = mok.AdamwTensors([])
     _step(lst, Stream(7))

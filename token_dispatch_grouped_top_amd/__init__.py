@@ -361,10 +361,13 @@ class AdamwTensors:
             c.n, c.grad_type = n, _TYPES[t["grad"].dtype]
             c.state_format = MOK_STATE_MXFP8 if coded else MOK_STATE_F32
             c.lr_scale, c.weight_decay = t.get("lr_scale", 1.0), t.get("weight_decay", 0.0)
-        self.plan, self.table, self.address, self.streams = mok_adamw_plan(), None, 0, set()
+        self.plan, self.table, self.address = mok_adamw_plan(), None, 0
+        self.device, self.streams = device, set()
         if self.tensors:
             size = mok_adamw_table_size(len(self.c))
             on, captured = _stream_object(stream), torch.cuda.is_current_stream_capturing()
+            if on.device.index != device:
+                raise ValueError(f"stream: of {on.device}, which is not the current GPU")
             # memory of the stream that writes it: a block of another stream's may still have work pending there
             with torch.cuda.stream(on):
                 if captured and not torch.cuda.is_current_stream_capturing():
@@ -411,7 +414,10 @@ def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float,
             raise ValueError("scalars: 16 dense bytes are wanted")
         scalars = _buffer(scalars, "scalars", (scalars.dtype,), 16 // size, _device())
     h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
-    on = _stream_of(stream, _device())
+    device = _device()
+    if tensors.device != device and tensors.address:
+        raise ValueError(f"tensors: a list on cuda:{tensors.device}, which is not the current GPU")
+    on = _stream_of(stream, device)
     if on not in tensors.streams:                 # once for each stream but the one that the list was built under
         tensors.record_stream(stream)
     _check(_lib.mok_adamw_step(tensors.address, C.byref(tensors.plan), C.byref(h), scalars or 0, on),
