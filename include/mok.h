@@ -189,8 +189,9 @@ typedef struct {
  * behind its picks (mok_build_schedule and the fused layer pass over them).
  * The order is that of c (without a bias: of the logits, which is the same)
  * and of the group values, evaluated in fp64 where fp32 cannot tell; two that
- * differ by less than 2^-48 of them, and not by nothing, may come in either
- * order.
+ * differ by less than 2^-48 (softmax with a bias: 2^-45, for the rounding of
+ * its sum over E) of the largest of them and of the scores in them, and not by
+ * nothing, may come in either order.
  * load (int32 [E], or NULL): the number of tokens that picked each expert is
  * added to it.  Every pointer is aligned for its elements.  T up to 2^26 - 4
  * (MOK_ERR_UNSUPPORTED), here and in the two calls that follow from it. */

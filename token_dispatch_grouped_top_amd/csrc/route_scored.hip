@@ -13,7 +13,8 @@
 //      t0 less twice the error: all that could be among the k largest c, seldom more than
 //      k + 1;
 //   2. the candidates, one to a lane, get c in fp64, and each counts the
-//      candidates before it, which is its place among the picks.
+//      candidates before it, by all bits of c and the lane, which is its place
+//      among the picks.
 // Groups are ranked by fp32 values; where the values at the border are nearer
 // than their error, the groups' values are formed in fp64 (exact_groups).
 // Where more candidates are left than lanes (many equal logits), the wave takes
@@ -263,20 +264,24 @@ __device__ __forceinline__ int exact_picks(const RouterArgs& r, const void* __re
   return mine;
 }
 
-// How many lanes of the token's row of 16 hold a larger value (kL = 16).
+// How many lanes of the token's row of 16 come before this one by (value, lane)
+// (kL = 16).  The source of row_ror:R is below lane sl if sl >= R.
 template <int R>
-__device__ __forceinline__ int count_before16(double v) {
-  if constexpr (R == 16) return 0;
-  else return (dpp<0x120 + R>(v) > v ? 1 : 0) + count_before16<R + 1>(v);   // row_ror:R
+__device__ __forceinline__ int count_before16(double v, int sl) {
+  if constexpr (R == 16) {
+    return 0;
+  } else {
+    const double o = dpp<0x120 + R>(v);
+    return ((o > v) | ((o == v) & (sl >= R)) ? 1 : 0) + count_before16<R + 1>(v, sl);
+  }
 }
 
-// Groups before this lane's by (value, id), where every lane holds its group's
-// value and kM lanes are a group: rotations by whole groups.  The source of
-// row_ror:R is below lane sl if sl >= R.
+// The same for keys, where kM lanes are a group that holds one key: the groups
+// before this lane's, by rotations by whole groups.
 template <int kM, int R>
-__device__ __forceinline__ int groups_before16(int own, int sl) {
+__device__ __forceinline__ int count_before16(int own, int sl) {
   if constexpr (R >= 16) return 0;
-  else return (dpp<0x120 + R>(own) > own - (sl >= R ? 1 : 0) ? 1 : 0) + groups_before16<kM, R + kM>(own, sl);
+  else return (dpp<0x120 + R>(own) > own - (sl >= R ? 1 : 0) ? 1 : 0) + count_before16<kM, R + kM>(own, sl);
 }
 
 // Whether the lane's group is among the top_groups, from values in fp64 of the
@@ -451,10 +456,10 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     const int gk = counts ? key_of(gv) : kNoKey;
     int before = 0;
     if constexpr (kL == 16) {
-      if (r.log_m == 0) before = groups_before16<1, 1>(gk, w.sl);
-      else if (r.log_m == 1) before = groups_before16<2, 2>(gk, w.sl);
-      else if (r.log_m == 2) before = groups_before16<4, 4>(gk, w.sl);
-      else before = groups_before16<8, 8>(gk, w.sl);
+      if (r.log_m == 0) before = count_before16<1, 1>(gk, w.sl);
+      else if (r.log_m == 1) before = count_before16<2, 2>(gk, w.sl);
+      else if (r.log_m == 2) before = count_before16<4, 4>(gk, w.sl);
+      else before = count_before16<8, 8>(gk, w.sl);
     } else {
       for (int g = 0; g < r.G; ++g) {
         const int o = lane_value(gk, g << r.log_m);
@@ -567,19 +572,16 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
   {
     double v = kNegInf64;
     if (e >= 0) v = bias ? s + static_cast<double>(be) : static_cast<double>(le);
-    // equal values in id order, which is lane order: the lane's number in the last bits (the larger
-    // value for the lower lane, of either sign)
-    if (e >= 0) {
-      const uint64_t u = __builtin_bit_cast(uint64_t, v == 0.0 ? 0.0 : v);
-      const uint64_t low = static_cast<uint64_t>((u >> 63) ? w.sl : kL - 1 - w.sl);
-      v = __builtin_bit_cast(double, (u & ~static_cast<uint64_t>(kL - 1)) | low);
-    }
+    // all bits of v count; equal values in id order, which is lane order
     if constexpr (kL == 16) {
-      place = count_before16<1>(v);
+      place = bias ? count_before16<1>(v, w.sl) : count_before16<1, 1>(key_of(le), w.sl);
     } else {
       place = 0;
       const int n = n_cand < kL ? n_cand : kL;
-      for (int j = 0; j < n; ++j) place += lane_value(v, j) > v ? 1 : 0;
+      for (int j = 0; j < n; ++j) {
+        const double o = lane_value(v, j);
+        place += (o > v) | ((o == v) & (j < w.sl)) ? 1 : 0;
+      }
     }
   }
   if (__ballot(plain)) {
