@@ -12,6 +12,7 @@
 
 #include "mok_internal.h"
 #include "persistent.h"
+#include "scored_adamw.h"
 
 namespace mok {
 namespace {

@@ -32,7 +32,7 @@
 // 8-bit codes follow from the bits of m and v.
 #include <cmath>
 
-#include "mok_internal.h"
+#include "scored_adamw.h"
 
 namespace mok {
 

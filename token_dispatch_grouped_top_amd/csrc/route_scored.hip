@@ -37,7 +37,7 @@
 // are in id order.
 #include <type_traits>
 
-#include "mok_internal.h"
+#include "scored_adamw.h"
 
 namespace mok {
 
