@@ -678,7 +678,8 @@ typedef struct {
  * steps, on any stream that comes after the writing, as long as the tensors
  * stay where they are.  No two buffers that a step writes may overlap;
  * overlapping p are refused (MOK_ERR_INVALID_ARG), and so are lists of more than
- * 2^24 units of 1024 elements (MOK_ERR_UNSUPPORTED).  fp32 pointers must be
+ * 2^24 - 1 units of one state format (MOK_ERR_UNSUPPORTED): 1024 elements of a
+ * tensor, 2048 with 8-bit states, its last unit may be shorter.  fp32 pointers must be
  * 4-byte, bf16 pointers 2-byte aligned; tensors whose pointers are all aligned
  * for 4 elements (16 bytes of fp32) go faster. */
 typedef struct {

@@ -291,7 +291,7 @@ mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tens
                                  size_t table_bytes, mok_adamw_plan* plan, hipStream_t stream) {
   if (n_tensors < 0 || !plan || (n_tensors > 0 && (!tensors || !table))) return MOK_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(table) % 16 != 0) return MOK_ERR_INVALID_ARG;
-  int64_t units = 0;
+  int64_t units[2] = {0, 0};                    // of fp32 states, of 8-bit states
   try {
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // [begin, end) of every p
     spans.reserve(n_tensors);
@@ -303,9 +303,10 @@ mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tens
       if (x.state_format != MOK_STATE_F32 && x.state_format != MOK_STATE_MXFP8)
         return MOK_ERR_INVALID_ARG;
       if (x.n == 0) continue;
-      if (x.n > adamw_max_elements()) return MOK_ERR_UNSUPPORTED;
-      units += x.n / 1024 + 1;
       const bool mx = x.state_format == MOK_STATE_MXFP8;
+      const int64_t own = adamw_units(x.n, mx);
+      if (own > kAdamwMaxUnits) return MOK_ERR_UNSUPPORTED;
+      units[mx] += own;
       if (!x.p || !x.grad || !x.m || !x.v || (mx && (!x.m_scale || !x.v_scale)))
         return MOK_ERR_INVALID_ARG;
       if (odd(x.p, 4) || odd(x.p_bf16, 2) || odd(x.grad, type_size(x.grad_type)) ||
@@ -320,7 +321,7 @@ mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tens
   } catch (const std::bad_alloc&) {
     return MOK_ERR_UNSUPPORTED;
   }
-  if (units > kAdamwMaxUnits) return MOK_ERR_UNSUPPORTED;   // one launch's grid
+  if (std::max(units[0], units[1]) > kAdamwMaxUnits) return MOK_ERR_UNSUPPORTED;   // a launch's grid
   if (n_tensors > 0 && table_bytes < adamw_table_bytes(n_tensors)) return MOK_ERR_WORKSPACE;
   *plan = mok_adamw_plan{};
   return hip_status(launch_adamw_table(tensors, n_tensors, table, *plan, stream));

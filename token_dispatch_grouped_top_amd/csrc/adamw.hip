@@ -468,7 +468,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 size_t adamw_table_bytes(int64_t n) { return descriptors_at(n) + static_cast<size_t>(n) * sizeof(TensorArg); }
 
-int64_t adamw_max_elements() { return kAdamwMaxUnits * kGroup; }
+int64_t adamw_units(int64_t n, bool mx) { return (n - 1) / (kGroup * (mx ? kMxGroups : 1)) + 1; }
 
 hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* table,
                               mok_adamw_plan& plan, hipStream_t s) {
@@ -478,7 +478,6 @@ hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* 
   a.first = a.count = 0;
   plan.list = n;
   for (int mx = 0; mx < 2; ++mx) {                      // the tensors of each format follow each other
-    const int64_t size = static_cast<int64_t>(kGroup) * (mx ? kMxGroups : 1);
     for (int32_t i = 0; i < n; ++i) {
       const mok_adamw_tensor& x = tensors[i];
       if (x.n == 0 || (x.state_format == MOK_STATE_MXFP8) != (mx == 1)) continue;
@@ -489,7 +488,7 @@ hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* 
       a.t[a.count++] = TensorArg{x.p, static_cast<uint16_t*>(x.p_bf16), x.grad, x.m, x.v, x.m_scale,
                                  x.v_scale, x.n, (bf16 ? kBf16Grad : 0) | (wide ? kWide : 0),
                                  static_cast<uint32_t>(i), x.lr_scale, x.weight_decay, plan.n_units[mx]};
-      plan.n_units[mx] += (x.n + size - 1) / size;
+      plan.n_units[mx] += adamw_units(x.n, mx);
       ++plan.n_tensors[mx];
       if (a.count == kBatch) {
         hipLaunchKernelGGL(k_adamw_table, dim3(1), dim3(kWave), 0, s, a, units, out);

@@ -23,10 +23,10 @@ hipError_t launch_route_scored_bwd(const RouterArgs& r, const void* logits, bool
 hipError_t launch_bias_update(int32_t* load, int32_t n_layers, int32_t E, float rate, float* bias,
                               bool clear_load, hipStream_t s);
 
-// AdamW over a list of tensors (checked; none above adamw_max_elements): the
+// AdamW over a list of tensors (checked): the units of a tensor (n > 0), the
 // table's bytes, its writing, and the step.
 constexpr int64_t kAdamwMaxUnits = (1 << 24) - 1;   // workgroups of a launch (2^32 threads)
-int64_t adamw_max_elements();
+int64_t adamw_units(int64_t n, bool mx);
 size_t adamw_table_bytes(int64_t n);
 hipError_t launch_adamw_table(const mok_adamw_tensor* tensors, int32_t n, void* table,
                               mok_adamw_plan& plan, hipStream_t s);
