@@ -676,7 +676,8 @@ typedef struct {
  * the host list (read before the call returns), and a plan of its units, which
  * the host keeps (private to the library).  Table and plan serve any number of
  * steps, on any stream that comes after the writing, as long as the tensors
- * stay where they are.  No two buffers that a step writes may overlap;
+ * stay where they are; the table is not freed or written before they are done.
+ * No two buffers that a step writes may overlap;
  * overlapping p are refused (MOK_ERR_INVALID_ARG), and so are lists of more than
  * 2^24 - 1 units of one state format (MOK_ERR_UNSUPPORTED): 1024 elements of a
  * tensor, 2048 with 8-bit states, its last unit may be shorter.  fp32 pointers must be

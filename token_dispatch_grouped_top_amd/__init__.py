@@ -330,8 +330,8 @@ class AdamwTensors:
     and ``weight_decay`` (0).  Dense tensors of the same number of elements on one GPU.  Built
     once for a program's buffers, on the stream given, which is waited for: the list can then be
     used on any stream.  Built during a capture, on a captured stream, it serves the steps of that
-    graph, which writes the table anew on each replay.  A program that lets torch allocate new gradients
-    for a step builds a new list for them.
+    graph, which writes the table anew on each replay.  A program that lets torch allocate new
+    gradients for a step builds a new list for them: 35 us for one tensor, 3 us for each more.
 
     A list may be dropped while a step of it runs, on any stream (a stream given as a raw handle
     lives as long as the list).  The tensors themselves are those of the current stream, as for

@@ -17,18 +17,25 @@
 //      among the picks.
 // Groups are ranked by fp32 values; where the values at the border are nearer
 // than their error, the groups' values are formed in fp64 (exact_groups).
-// Where more candidates are left than lanes (many equal logits), the wave takes
-// the plain way (exact_picks): fp64 for every expert and k rounds of argmax.
+// Where more candidates are left than lanes, the wave takes the plain way
+// (exact_picks): fp64 for every expert and k rounds of argmax.  That is so with
+// many equal logits; and as a lane keeps its four largest keys, with any logits
+// where the open groups' lanes keep fewer than k in all (4 m top_groups < k, m the
+// lanes of a group), and now and then where they keep little more.
 // Reductions over lanes are of integers in the floats' order: one DPP
 // instruction a level.
 //
-// Bound by the issue of vector instructions, not by HBM: 780 a wave of four
-// tokens over 256 experts (a key takes 15, the rest is the same for any number).
-// 16384 tokens in 8 groups 8.8 us, 65536 23.8 us (their logits alone take 3.2 and
-// 13 us at the rate of a large copy); 384 experts without groups 9.5 and 28.8 us.
-// One token 4.1 us, half of it the launch.  (A first version with an fp64 score
-// of every logit, k rounds of argmax over 64 lanes and an atomic for each pick
-// took 174 us for the 16384 tokens with their load; now 11.5.)
+// Times over four sets of buffers in turn.  65536 tokens, 256 experts in 8 groups,
+// 27.6 us: bound by the issue of vector instructions, 760 a wave of four tokens (a
+// key takes 15, the rest is the same for any number of experts; the logits alone
+// take 13 us at the rate of a large copy).  16384 tokens 11.7 us, of which 5.1 are
+// issue, 3.3 the logits and 1.9 the launch, one after the other: four waves a SIMD
+// start together and each loads, computes, stores.  384 experts without groups
+// 11.9 and 34.9 us, 73728 tokens 38.5.  One token 4.1 us, half of it the launch.
+// The plain way: 16384 tokens over 256 experts with all logits equal 53 us; over
+// 512 in 8 groups, k = 12, four open 17.7 us, two 59 (some waves), one 100 (all).
+// (A first version with an fp64 score of every logit, k rounds of argmax over 64
+// lanes and an atomic for each pick took 174 us for 16384 tokens with their load.)
 //
 // Lanes.  A token has kL = 16 or 64 lanes.  Every group of experts gets m
 // neighbouring lanes (the largest power of two with m G <= kL), each a run of
@@ -55,10 +62,16 @@ constexpr double kNegInf64 = -__builtin_inf();
 constexpr float kSigmoidErr = 0x1p-22f, kSoftmaxErr = 0x1p-21f;
 constexpr float kRel = 0x1p-23f;
 constexpr float kLog2e = 1.44269504f;
-// Tokens from which four share a wave: forward (384 experts, 16 against 64 lanes
-// a token: 2048 tokens 4.6 and 4.7 us, 16384 9.5 and 17.2), sparse backward (256
-// experts in bf16: 4096 tokens 3.5 and 3.35 us, 16384 4.8 and 7.0), dense
-// backward (16384 10.3 and 9.4 us, 65536 29.0 and 27.6; 160 experts 21.7 and 25.8).
+// Tokens from which four share a wave, 16 lanes a token against 64 (us, buffers in
+// turn).  Forward: 2048 tokens over 160 experts 4.55 and 5.0, 256 5.3 and 5.4, 384
+// 4.8 and 5.0, 512 6.2 and 5.0; 16384 tokens 8.0 and 17.9, 10.5 and 19.7, 11.2 and
+// 19.0, 16.1 and 19.2 (512 gain from 4096 tokens on).  Sparse backward, fp32: 256
+// experts, 4096 tokens 3.6 and 3.5, 8192 4.6 and 4.9, 16384 7.3 and 8.6; 512
+// experts 4.3 and 4.1, 6.9 and 6.7, 9.4 and 10.1.  Dense backward, fp32: 160
+// experts, 16384 tokens 9.0 and 9.1, 32768 13.7 and 14.6, 65536 22.2 and 25.8; 256
+// experts 10.8 and 9.7, 16.2 and 15.1, 32.6 and 35.2 (bf16 13.9 and 15.2 at 32768);
+// above 256 experts 64 lanes are faster at every size: 384 experts 30.8 and 27.6 at
+// 32768, 512 35.4 and 29.3.
 constexpr int kManyTokens = 2048, kManySparse = 8192, kManyDense = 32768;
 // Picks up to which each adds to the load by itself: about 1 ns a pick on the
 // same few lines, against a second launch of 2.2 to 3 us.
@@ -656,11 +669,11 @@ void k_load_count(const int32_t* __restrict__ idx, int64_t n, int32_t E, int32_t
 // (softmax without renorm): with the picks' weights w in the row,
 //   D = sum_e s_e w_e,  dl_e = s_e (w_e - D),
 // the logits in registers, V of them to a lane, four neighbours at a time.
-// Bound by the row's write (and for the dense form its read): 16384 tokens over
-// 256 experts sparse 6.1 us in fp32, 4.8 in bf16, dense 9.4 and 8.6; 65536 sparse
-// 18.1 us (3.7 TB/s).  Zeros written before the picks' values instead of a row in
-// LDS: 3.6 us where this takes 3.7 at 4096 tokens, 19.7 where it takes 18.1 at
-// 65536.
+// Bound by the row's write (and for the dense form its read).  Buffers in turn,
+// 256 experts: 16384 tokens sparse 7.4 us in fp32, 6.1 in bf16, dense 9.9 and 9.6;
+// 65536 sparse 25.5 us, dense 31.2.  Zeros written before the picks' values instead
+// of a row in LDS, over the same buffers again and again: 3.6 us where this takes
+// 3.7 at 4096 tokens, 19.7 where it takes 18.1 at 65536.
 template <int kL, int V, bool BF16>
 __global__ __launch_bounds__(kWaves * kWave)
 void k_route_scored_bwd(RouterArgs r, const void* __restrict__ logits, int64_t ld, int32_t T,
