@@ -278,26 +278,27 @@ __device__ __forceinline__ int exact_picks(const RouterArgs& r, const void* __re
 }
 
 // How many of lanes [kFrom, kTo) of the token's row of 16 come before this one by
-// (value, lane).  16384 tokens over 256 experts with load 12.85 us, 65536 over 256
-// 22.9, 73728 over 384 36.8; with 15 rotations in place of the lanes that hold a
-// candidate 13.05, 23.6 and 37.7.
-template <int kFrom, int kTo>
-__device__ __forceinline__ int count_of16(double v, int sl) {
+// (value, lane).  Both launches of 16384 tokens over 256 experts with load 12.8 us,
+// 65536 over 256 22.9, 73728 over 384 36.8; with 15 rotations in place of the lanes
+// that hold a candidate 13.05, 23.6 and 37.7 (keys, without a bias: 65536 over 256
+// 19.0 and 19.4).
+template <int kFrom, int kTo, class T>
+__device__ __forceinline__ int count_of16(T v, int sl) {
   if constexpr (kFrom == kTo) {
     return 0;
   } else {
-    const double o = dpp<0x150 + kFrom>(v);               // row_newbcast:kFrom
+    const T o = dpp<0x150 + kFrom>(v);                    // row_newbcast:kFrom
     return ((o > v) | ((o == v) & (sl > kFrom)) ? 1 : 0) + count_of16<kFrom + 1, kTo>(v, sl);
   }
 }
 
-// The same for keys, where kM lanes are a group that holds one key: the groups
-// before this lane's, by rotations by whole groups.  The source of row_ror:R is
-// below lane sl if sl >= R.
+// Groups before this lane's by (value, id), where every lane holds its group's
+// value and kM lanes are a group: rotations by whole groups.  The source of
+// row_ror:R is below lane sl if sl >= R.
 template <int kM, int R>
-__device__ __forceinline__ int count_before16(int own, int sl) {
+__device__ __forceinline__ int groups_before16(int own, int sl) {
   if constexpr (R >= 16) return 0;
-  else return (dpp<0x120 + R>(own) > own - (sl >= R ? 1 : 0) ? 1 : 0) + count_before16<kM, R + kM>(own, sl);
+  else return (dpp<0x120 + R>(own) > own - (sl >= R ? 1 : 0) ? 1 : 0) + groups_before16<kM, R + kM>(own, sl);
 }
 
 // Whether the lane's group is among the top_groups, from values in fp64 of the
@@ -472,10 +473,10 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     const int gk = counts ? key_of(gv) : kNoKey;
     int before = 0;
     if constexpr (kL == 16) {
-      if (r.log_m == 0) before = count_before16<1, 1>(gk, w.sl);
-      else if (r.log_m == 1) before = count_before16<2, 2>(gk, w.sl);
-      else if (r.log_m == 2) before = count_before16<4, 4>(gk, w.sl);
-      else before = count_before16<8, 8>(gk, w.sl);
+      if (r.log_m == 0) before = groups_before16<1, 1>(gk, w.sl);
+      else if (r.log_m == 1) before = groups_before16<2, 2>(gk, w.sl);
+      else if (r.log_m == 2) before = groups_before16<4, 4>(gk, w.sl);
+      else before = groups_before16<8, 8>(gk, w.sl);
     } else {
       for (int g = 0; g < r.G; ++g) {
         const int o = lane_value(gk, g << r.log_m);
@@ -590,14 +591,14 @@ void k_route_scored(RouterArgs r, const void* __restrict__ logits, int64_t ld,
     if (e >= 0) v = bias ? s + static_cast<double>(be) : static_cast<double>(le);
     // all bits of v count; equal values in id order, which is lane order
     if constexpr (kL == 16) {
-      if (bias) {
-        place = count_of16<0, 8>(v, w.sl);
-        const uint64_t any = __ballot(e >= 0);            // seldom many more candidates than k
-        if (any & 0xff00ff00ff00ff00ull) place += count_of16<8, 12>(v, w.sl);
-        if (any & 0xf000f000f000f000ull) place += count_of16<12, 16>(v, w.sl);
-      } else {
-        place = count_before16<1, 1>(key_of(le), w.sl);
-      }
+      const uint64_t any = __ballot(e >= 0);              // seldom many more candidates than k
+      const auto count = [&](auto x) {
+        int n = count_of16<0, 8>(x, w.sl);
+        if (any & 0xff00ff00ff00ff00ull) n += count_of16<8, 12>(x, w.sl);
+        if (any & 0xf000f000f000f000ull) n += count_of16<12, 16>(x, w.sl);
+        return n;
+      };
+      place = bias ? count(v) : count(key_of(le));
     } else {
       place = 0;
       const int n = n_cand < kL ? n_cand : kL;
