@@ -28,7 +28,7 @@
 // Times over four sets of buffers in turn.  65536 tokens, 256 experts in 8 groups,
 // 27.6 us: bound by the issue of vector instructions, 760 a wave of four tokens (a
 // key takes 15, the rest is the same for any number of experts; the logits alone
-// take 13 us at the rate of a large copy).  16384 tokens 11.7 us, of which 5.1 are
+// take 13 us at the rate of a large copy).  16384 tokens 11.2 us, of which 5.1 are
 // issue, 3.3 the logits and 1.9 the launch, one after the other: four waves a SIMD
 // start together and each loads, computes, stores.  384 experts without groups
 // 11.9 and 34.9 us, 73728 tokens 38.5.  One token 4.1 us, half of it the launch.
