@@ -614,6 +614,113 @@ mok_status mok_dispatch_backward(const void* dx_slots, int32_t rows,
                                  hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Products in 8 bits with a scale for each block of 128 (the format of 8-bit
+ * checkpoints and training runs that keep fp32 scales; the MXFP8 calls above
+ * have E8M0 scales for 32 values).  A value is code * scale, the code E4M3
+ * (OCP, bias 7, largest 448, 0x7f / 0xff NaN).  Operands:
+ *   token operand   codes u8 [rows][K], row-major; scales fp32
+ *                   [ceil(K / 128)][rows]: one for 128 values of a row, block
+ *                   j of row r at j * rows + r
+ *   weight operand  codes u8 [N][K], row-major; scales fp32
+ *                   [ceil(N / 128)][ceil(K / 128)]: one for 128 x 128 values
+ * K and N are multiples of 64, so a last block may be 64 wide.  Codes are
+ * 16-byte aligned, scales 4-byte.
+ * Slot blocks: for products that contract over an expert's rows (the weight
+ * gradients) operands lie transposed, codes [W][S] with S =
+ * mok_block8_slots(rows, n_local): expert e's rows offsets[e] ..
+ * offsets[e+1] - 1 begin at place 128 * sum_{e' < e} ceil(count_e' / 128) and
+ * are followed by zeros up to a multiple of 128.
+ * Here offsets may be NULL with n_local = 1: all `rows` rows are one
+ * expert's.  Rows at and past min(offsets[n_local], rows), and places behind
+ * the last expert's, are neither read nor written.
+ * ------------------------------------------------------------------------ */
+
+/* What a quantiser reads, W values a row:
+ *   MOK_BLOCK8_COPY        x[r][c]
+ *   MOK_BLOCK8_SWIGLU      SiLU(g) u with g = x[r][c], u = x[r][W + c] (x: h =
+ *                          [g, u], 2 W wide)
+ *   MOK_BLOCK8_SWIGLU_BWD  [dg, du] of SwiGLU's backward, W = 2 I: with g =
+ *                          x[r][c], u = x[r][I + c] (x: h) and da = d[r][c] (d: I
+ *                          wide), dg = da u s (1 + g (1 - s)) in column c, du =
+ *                          da g s in column I + c, s = 1 / (1 + e^-g)
+ * (fp32 arithmetic). */
+typedef enum {
+    MOK_BLOCK8_COPY = 0, MOK_BLOCK8_SWIGLU = 1, MOK_BLOCK8_SWIGLU_BWD = 2
+} mok_block8_op;
+
+/* Scales of the transposed codes: one for 128 slots of a column (a token
+ * operand of mok_block8_wgrad), or for 128 slots x 128 columns (its weight
+ * operand). */
+typedef enum { MOK_BLOCK8_LINES = 0, MOK_BLOCK8_BLOCKS = 1 } mok_block8_scales;
+
+typedef struct {
+    int32_t op;          /* mok_block8_op                                        */
+    int32_t type;        /* mok_type of x and d                                  */
+    const void* x;
+    int64_t ld;          /* elements between rows of x; >= its width             */
+    const void* d;       /* MOK_BLOCK8_SWIGLU_BWD                                */
+    int64_t ldd;
+    int32_t ring_rows;   /* 0: x is row-major; else (bf16, MOK_BLOCK8_COPY) x is
+                            column-blocked, a ring of ring_rows rows, row r at
+                            r % ring_rows (what mok_dispatch_gather and
+                            mok_combine_backward write); ld is not read          */
+    int32_t reserved;    /* 0 */
+} mok_block8_source;
+
+/* Number of places of a transposed operand's rows: 128 * (ceil(rows / 128) +
+ * n_local - 1); 0 for bad arguments.  Host only. */
+int64_t mok_block8_slots(int32_t rows, int32_t n_local);
+
+/* Quantiser of token rows.  For each block, scale = max(amax / 448, 2^-126) in
+ * fp32 (amax: its largest finite magnitude), code = the E4M3 value nearest to
+ * the fp32 quotient value / scale, in the middle the even one, at most 448; a
+ * value that is not finite becomes the code 0xff (NaN) and does not enter the
+ * scale.
+ *   codes, scales      the rows as a token operand with K = W
+ *   codes_t, scales_t  the slot blocks [W][S]; t_scales (mok_block8_scales) says
+ *                      of which kind: LINES: scales_t fp32 [S / 128][W], BLOCKS:
+ *                      scales_t fp32 [ceil(W / 128)][S / 128]
+ * Either pair may be NULL.  One pass over the source. */
+mok_status mok_block8_quantise(const mok_block8_source* src, int32_t rows, int32_t W,
+                               const int32_t* offsets, int32_t n_local, uint8_t* codes,
+                               float* scales, uint8_t* codes_t, float* scales_t, int32_t t_scales,
+                               hipStream_t stream);
+
+/* Quantiser of weights: n matrices [N][K] (mok_type, dense) as weight operands
+ * [n][N][K], with scales [n][ceil(N / 128)][ceil(K / 128)] by the rule above;
+ * codes_t / scales_t (both or neither NULL): the same values as the transposed
+ * matrices' operand, codes [n][K][N], scales [n][ceil(K / 128)][ceil(N / 128)]
+ * (what the gradient of the product's input takes). */
+mok_status mok_block8_quantise_weights(const void* w, int32_t type, int32_t n, int32_t N, int32_t K,
+                                       uint8_t* codes, float* scales, uint8_t* codes_t,
+                                       float* scales_t, hipStream_t stream);
+
+/* Grouped product: for each row r of expert e
+ *   out[r][i] = sum_j a_scale[j][r] w_scale[e][i / 128][j] sum_{k in block j} a[r][k] w[e][i][k]
+ * (out_type, [rows][N] dense), summed in fp32 over a block, then over the blocks
+ * in ascending order.  A result in bf16 comes from the 8-bit matrix
+ * instructions, which drop of every 64 products what is below 2^-13 of the
+ * largest; one in fp32 from fp16's, exact to fp32 and slower.  n_local expert matrices [n_local][N][K] as
+ * mok_block8_quantise_weights leaves them.  A block's two scales multiplied
+ * have to stay within fp32's range.  K up to 2^20, N * K below 2^32. */
+mok_status mok_block8_gemm(const uint8_t* a, const float* a_scales, int32_t rows, int32_t K,
+                           const int32_t* offsets, int32_t n_local, const uint8_t* w,
+                           const float* w_scales, int32_t N, void* out, int32_t out_type,
+                           hipStream_t stream);
+
+/* Weight gradients from slot blocks: for each expert e
+ *   dw[e][i][j] = sum over e's slot blocks b of dy_scale[b][i] x_scale[j / 128][b]
+ *                 sum_{s in b} dy_t[i][s] x_t[j][s]
+ * dy_t: LINES [M][S], x_t: BLOCKS [N][S], both as mok_block8_quantise writes
+ * them for `rows` and n_local; M and N multiples of 64; dw [n_local][M][N]
+ * (out_type, summed as by mok_block8_gemm).  accumulate = 1 (fp32 dw): added to dw.  An expert without rows
+ * gets zeros, or keeps its dw. */
+mok_status mok_block8_wgrad(const uint8_t* dy_t, const float* dy_scales, int32_t M,
+                            const uint8_t* x_t, const float* x_scales, int32_t N, int32_t rows,
+                            const int32_t* offsets, int32_t n_local, void* dw, int32_t out_type,
+                            int32_t accumulate, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * AdamW over many tensors at once (the step that follows the weight gradients
  * above).  Per element, with g = grad * grad_scale and t the step:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
@@ -698,6 +805,56 @@ mok_status mok_adamw_build_table(const mok_adamw_tensor* tensors, int32_t n_tens
 mok_status mok_adamw_step(const void* table, const mok_adamw_plan* plan,
                           const mok_adamw_hyper* hyper, const mok_adamw_scalars* scalars,
                           hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates of matrices (Muon): n matrices of one shape, each
+ * [rows][cols], dense, one behind the other.  With v a matrix whose smaller
+ * side comes first (transposed, if rows > cols):
+ *   X = v / |v|_F,  then `steps` times  X = a X + (b G + c G^2) X,  G = X X^T,
+ * which moves every singular value towards 1 where (a, b, c) are chosen for it
+ * ((3.4445, -4.7750, 2.0315) and 5 steps: to between 0.7 and 1.2).  The norm is
+ * formed in fp64; X, G and b G + c G^2 are held in fp16, the products' sums in
+ * fp32: the result is off by about 2^-10 of its root mean square.  A zero
+ * matrix stays zero; one that holds a value that is not finite becomes NaN,
+ * the others do not.  Coefficients with which X leaves [-200, 200] overflow.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    float a, b, c;       /* finite                                               */
+    int32_t steps;       /* 1..32                                                */
+} mok_newton_schulz;
+
+/* Bytes of scratch of the two calls below; 0 for bad sizes.  rows and cols up
+ * to 32768, n up to 65535.  Contents on entry do not matter. */
+size_t mok_muon_workspace_size(int32_t n, int32_t rows, int32_t cols);
+
+/* out (bf16 [n][rows][cols]) = the orthogonalised x (mok_type, same shape).
+ * They may not overlap. */
+mok_status mok_orthogonalise(const void* x, int32_t type, int32_t n, int32_t rows, int32_t cols,
+                             const mok_newton_schulz* ns, void* out, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+typedef struct {
+    double lr, momentum;     /* 0 <= momentum < 1                                */
+    double weight_decay;
+    double grad_scale;       /* factor of every gradient                         */
+    double scale;            /* factor of the orthogonalised update              */
+    int32_t nesterov;        /* 0 or 1                                           */
+    int32_t reserved;        /* 0 */
+    mok_newton_schulz ns;
+} mok_muon_hyper;
+
+/* One step, in place (fp32, the factors formed in fp64):
+ *   g = grad * grad_scale;  m = momentum m + g;  v = nesterov ? g + momentum m : m
+ *   p = p (1 - lr weight_decay) - lr scale X(v)
+ * p, m: fp32 [n][rows][cols]; grad: grad_type, same shape; p_bf16: NULL, or the
+ * new parameters rounded.  scalars: NULL, or device memory (16-byte aligned)
+ * whose lr and grad_scale are used in place of hyper's, and where skip != 0
+ * nothing is written (step is not read), as for mok_adamw_step.  No two
+ * buffers may overlap. */
+mok_status mok_muon_step(float* p, void* p_bf16, const void* grad, int32_t grad_type, float* m,
+                         int32_t n, int32_t rows, int32_t cols, const mok_muon_hyper* hyper,
+                         const mok_adamw_scalars* scalars, void* ws, size_t ws_bytes,
+                         hipStream_t stream);
 
 /* Bytes of workspace mok_moe_forward, mok_moe_forward_routed and
  * mok_moe_forward_batches need for T source tokens per macrobatch and n_macro

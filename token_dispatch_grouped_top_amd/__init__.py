@@ -38,6 +38,8 @@ MOK_TYPE_F32, MOK_TYPE_BF16 = 0, 1
 MOK_SCORE_SOFTMAX, MOK_SCORE_SIGMOID = 0, 1
 MOK_GROUP_MAX, MOK_GROUP_TOP2 = 0, 1
 MOK_STATE_F32, MOK_STATE_MXFP8 = 0, 1
+MOK_BLOCK8_COPY, MOK_BLOCK8_SWIGLU, MOK_BLOCK8_SWIGLU_BWD = 0, 1, 2
+MOK_BLOCK8_LINES, MOK_BLOCK8_BLOCKS = 0, 1
 
 
 class MokError(RuntimeError):
@@ -79,6 +81,21 @@ class mok_adamw_plan(C.Structure):
                 ("reserved", C.c_int32)]
 
 
+class mok_block8_source(C.Structure):
+    _fields_ = [("op", C.c_int32), ("type", C.c_int32), ("x", C.c_void_p), ("ld", C.c_int64),
+                ("d", C.c_void_p), ("ldd", C.c_int64), ("ring_rows", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class mok_newton_schulz(C.Structure):
+    _fields_ = [(n, C.c_float) for n in ("a", "b", "c")] + [("steps", C.c_int32)]
+
+
+class mok_muon_hyper(C.Structure):
+    _fields_ = [(n, C.c_double) for n in ("lr", "momentum", "weight_decay", "grad_scale", "scale")] + [
+        ("nesterov", C.c_int32), ("reserved", C.c_int32), ("ns", mok_newton_schulz)]
+
+
 _P, _I32, _I64, _SZ = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 _DESC, _TOK = C.POINTER(mok_layer_desc), C.POINTER(mok_tokens)
 _RTR = C.POINTER(mok_router_desc)
@@ -87,6 +104,17 @@ _SIGS = {
     "mok_route_scored": (C.c_int, [_RTR, _P, _I32, _I64, _P, _I32, _P, _P, _P, _P]),
     "mok_route_scored_backward": (C.c_int, [_RTR, _P, _I32, _I64, _I32, _P, _P, _P, _I64, _P]),
     "mok_route_bias_update": (C.c_int, [_P, _I32, _I32, C.c_float, _P, _I32, _P]),
+    "mok_block8_slots": (_I64, [_I32, _I32]),
+    "mok_block8_quantise": (C.c_int, [C.POINTER(mok_block8_source), _I32, _I32, _P, _I32, _P, _P, _P,
+                                      _P, _I32, _P]),
+    "mok_block8_quantise_weights": (C.c_int, [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P]),
+    "mok_block8_gemm": (C.c_int, [_P, _P, _I32, _I32, _P, _I32, _P, _P, _I32, _P, _I32, _P]),
+    "mok_block8_wgrad": (C.c_int, [_P, _P, _I32, _P, _P, _I32, _I32, _P, _I32, _P, _I32, _I32, _P]),
+    "mok_muon_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "mok_orthogonalise": (C.c_int, [_P, _I32, _I32, _I32, _I32, C.POINTER(mok_newton_schulz), _P, _P,
+                                    _SZ, _P]),
+    "mok_muon_step": (C.c_int, [_P, _P, _P, _I32, _P, _I32, _I32, _I32, C.POINTER(mok_muon_hyper), _P,
+                                _P, _SZ, _P]),
     "mok_adamw_table_size": (_SZ, [_I32]),
     "mok_adamw_build_table": (C.c_int, [C.POINTER(mok_adamw_tensor), _I32, _P, _SZ,
                                         C.POINTER(mok_adamw_plan), _P]),
@@ -321,6 +349,128 @@ def mok_route_bias_update(load, n_layers: int, E: int, rate: float, bias, clear_
                                       _stream_of(stream, device)), "mok_route_bias_update")
 
 
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def mok_block8_slots(rows: int, n_local: int = 1) -> int:
+    return int(_lib.mok_block8_slots(rows, n_local))
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _typed(x, name: str, n: int, device: int):
+    """(address, mok_type) of a dense fp32 or bf16 buffer of at least n elements (a raw address: fp32)."""
+    if x is None or type(x) is int:
+        return x or 0, MOK_TYPE_F32
+    return _buffer(x, name, tuple(_TYPES), n, device), _TYPES[x.dtype]
+
+
+def mok_block8_quantise(x, rows: int, W: int, codes=None, scales=None, source: int = MOK_BLOCK8_COPY,
+                        d=None, codes_t=None, scales_t=None, t_scales: int = MOK_BLOCK8_LINES,
+                        offsets=None, n_local: int = 1, ring_rows: int = 0, stream=None) -> None:
+    """x (and d): rows of fp32 or bf16, the rows themselves dense; or, with ring_rows, a dense bf16 buffer of
+    column-blocked rows.  codes: uint8 or float8_e4m3fn."""
+    device, s = _device(), mok_block8_source(op=source, ring_rows=ring_rows)
+    if ring_rows:
+        if not isinstance(x, int) and x is not None and x.dtype is torch.int16:
+            x = x.view(torch.bfloat16)
+        s.x, s.type = _buffer(x, "x", _BF16, ring_rows * W, device), MOK_TYPE_BF16
+    else:
+        s.x, s.type, s.ld = _rows(x, "x", rows, 2 * W if source == MOK_BLOCK8_SWIGLU else W, device)
+        if d is not None:
+            s.d, kind, s.ldd = _rows(d, "d", rows, W // 2, device)
+            if kind != s.type:
+                raise ValueError(f"d: {d.dtype} where x is {x.dtype}")
+    S = mok_block8_slots(rows, n_local)
+    n_scales = S // 128 * W if t_scales == MOK_BLOCK8_LINES else S // 128 * _blocks(W)
+    _check(_lib.mok_block8_quantise(C.byref(s), rows, W,
+                                    _buffer(offsets, "offsets", _I32S, n_local + 1, device), n_local,
+                                    _buffer(codes, "codes", _CODES, rows * W, device),
+                                    _buffer(scales, "scales", _F32, rows * _blocks(W), device),
+                                    _buffer(codes_t, "codes_t", _CODES, W * S, device),
+                                    _buffer(scales_t, "scales_t", _F32, n_scales, device), t_scales,
+                                    _stream_of(stream, device)), "mok_block8_quantise")
+
+
+def mok_block8_quantise_weights(w, n: int, N: int, K: int, codes, scales, codes_t=None, scales_t=None,
+                                stream=None) -> None:
+    device, blocks = _device(), n * _blocks(N) * _blocks(K)
+    at, kind = _typed(w, "w", n * N * K, device)
+    _check(_lib.mok_block8_quantise_weights(at, kind, n, N, K,
+                                            _buffer(codes, "codes", _CODES, n * N * K, device),
+                                            _buffer(scales, "scales", _F32, blocks, device),
+                                            _buffer(codes_t, "codes_t", _CODES, n * N * K, device),
+                                            _buffer(scales_t, "scales_t", _F32, blocks, device),
+                                            _stream_of(stream, device)), "mok_block8_quantise_weights")
+
+
+def mok_block8_gemm(a, a_scales, rows: int, K: int, w, w_scales, N: int, out, offsets=None,
+                    n_local: int = 1, stream=None) -> None:
+    device = _device()
+    to, kind = _typed(out, "out", rows * N, device)
+    _check(_lib.mok_block8_gemm(_buffer(a, "a", _CODES, rows * K, device),
+                                _buffer(a_scales, "a_scales", _F32, rows * _blocks(K), device), rows, K,
+                                _buffer(offsets, "offsets", _I32S, n_local + 1, device), n_local,
+                                _buffer(w, "w", _CODES, n_local * N * K, device),
+                                _buffer(w_scales, "w_scales", _F32, n_local * _blocks(N) * _blocks(K), device),
+                                N, to, kind, _stream_of(stream, device)), "mok_block8_gemm")
+
+
+def mok_block8_wgrad(dy_t, dy_scales, M: int, x_t, x_scales, N: int, rows: int, dw, offsets=None,
+                     n_local: int = 1, accumulate: int = 0, stream=None) -> None:
+    device, S = _device(), mok_block8_slots(rows, n_local)
+    to, kind = _typed(dw, "dw", n_local * M * N, device)
+    _check(_lib.mok_block8_wgrad(_buffer(dy_t, "dy_t", _CODES, M * S, device),
+                                 _buffer(dy_scales, "dy_scales", _F32, M * (S // 128), device), M,
+                                 _buffer(x_t, "x_t", _CODES, N * S, device),
+                                 _buffer(x_scales, "x_scales", _F32, _blocks(N) * (S // 128), device), N, rows,
+                                 _buffer(offsets, "offsets", _I32S, n_local + 1, device), n_local, to, kind,
+                                 accumulate, _stream_of(stream, device)), "mok_block8_wgrad")
+
+
+def mok_muon_workspace_size(n: int, rows: int, cols: int) -> int:
+    return int(_lib.mok_muon_workspace_size(n, rows, cols))
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def _workspace(ws, ws_bytes: Optional[int], device: int):
+    """(address, bytes) of a dense buffer on the GPU (a raw address: of ws_bytes)."""
+    if ws is None or type(ws) is int:
+        return ws or 0, ws_bytes or 0
+    size = ws.numel() * ws.element_size()
+    return _buffer(ws, "ws", (ws.dtype,), 0, device), size if ws_bytes is None else min(ws_bytes, size)
+
+
+def mok_orthogonalise(x, n: int, rows: int, cols: int, out, ws, steps: int = 5,
+                      coefficients: Sequence[float] = NEWTON_SCHULZ, ws_bytes: Optional[int] = None,
+                      stream=None) -> None:
+    device, cells = _device(), n * rows * cols
+    at, kind = _typed(x, "x", cells, device)
+    scratch, size = _workspace(ws, ws_bytes, device)
+    _check(_lib.mok_orthogonalise(at, kind, n, rows, cols, C.byref(mok_newton_schulz(*coefficients, steps)),
+                                  _buffer(out, "out", _BF16, cells, device), scratch, size,
+                                  _stream_of(stream, device)), "mok_orthogonalise")
+
+
+def mok_muon_step(p, grad, m, n: int, rows: int, cols: int, ws, lr: float, momentum: float, scale: float,
+                  weight_decay: float = 0.0, grad_scale: float = 1.0, nesterov: int = 1, steps: int = 5,
+                  coefficients: Sequence[float] = NEWTON_SCHULZ, p_bf16=None, scalars=None,
+                  ws_bytes: Optional[int] = None, stream=None) -> None:
+    """scalars: as for mok_adamw_step."""
+    device, cells = _device(), n * rows * cols
+    at, kind = _typed(grad, "grad", cells, device)
+    scratch, size = _workspace(ws, ws_bytes, device)
+    h = mok_muon_hyper(lr, momentum, weight_decay, grad_scale, scale, nesterov, 0,
+                       mok_newton_schulz(*coefficients, steps))
+    _check(_lib.mok_muon_step(_buffer(p, "p", _F32, cells, device), _buffer(p_bf16, "p_bf16", _BF16, cells, device),
+                              at, kind, _buffer(m, "m", _F32, cells, device), n, rows, cols, C.byref(h),
+                              _scalars(scalars), scratch, size, _stream_of(stream, device)), "mok_muon_step")
+
+
 class AdamwTensors:
     """Tensors of an AdamW step: the device table of ``mok_adamw_build_table``, its plan, and what
     keeps the tensors alive.
@@ -403,16 +553,22 @@ def mok_adamw_build_table(tensors, table, plan: mok_adamw_plan, stream=None) -> 
                                       C.byref(plan), _stream(stream)), "mok_adamw_build_table")
 
 
+def _scalars(x) -> int:
+    """Address of a mok_adamw_scalars: None, a raw address, or 16 dense bytes on the GPU."""
+    if x is not None and not isinstance(x, int):
+        size = x.element_size()
+        if x.numel() * size != 16:
+            raise ValueError("scalars: 16 dense bytes are wanted")
+        x = _buffer(x, "scalars", (x.dtype,), 16 // size, _device())
+    return x or 0
+
+
 def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float, eps: float,
                    step: int, grad_scale: float = 1.0, seed: int = 0, scalars=None,
                    stream=None) -> None:
     """scalars: None, or 16 bytes on the GPU as a ``mok_adamw_scalars`` (lr and grad_scale fp32,
     step and skip int32)."""
-    if scalars is not None and not isinstance(scalars, int):
-        size = scalars.element_size()
-        if scalars.numel() * size != 16:
-            raise ValueError("scalars: 16 dense bytes are wanted")
-        scalars = _buffer(scalars, "scalars", (scalars.dtype,), 16 // size, _device())
+    scalars = _scalars(scalars)
     h = mok_adamw_hyper(lr, beta1, beta2, eps, grad_scale, step, seed)
     device = _device()
     if tensors.device != device and tensors.address:
@@ -420,7 +576,7 @@ def mok_adamw_step(tensors: AdamwTensors, lr: float, beta1: float, beta2: float,
     on = _stream_of(stream, device)
     if on not in tensors.streams:                 # once for each stream but the one that the list was built under
         tensors.record_stream(stream)
-    _check(_lib.mok_adamw_step(tensors.address, C.byref(tensors.plan), C.byref(h), scalars or 0, on),
+    _check(_lib.mok_adamw_step(tensors.address, C.byref(tensors.plan), C.byref(h), scalars, on),
            "mok_adamw_step")
 
 

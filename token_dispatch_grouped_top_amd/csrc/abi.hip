@@ -1,7 +1,8 @@
 // abi.hip -- the extern "C" entry points of libmok: argument checks,
 // workspace carving and the stream-ordered orchestration of the fused layer.
 // The kernels live in route.hip, route_scored.hip, schedule.hip, movers.hip,
-// gemm.hip, wgrad.hip and adamw.hip; the persistent pipeline in persistent.hip.
+// gemm.hip, wgrad.hip, block8_quantise.hip, block8_gemm.hip, adamw.hip and
+// muon.hip; the persistent pipeline in persistent.hip.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -10,7 +11,9 @@
 #include <utility>
 #include <vector>
 
+#include "block8.h"
 #include "mok_internal.h"
+#include "muon.h"
 #include "persistent.h"
 #include "scored_adamw.h"
 
@@ -206,6 +209,23 @@ size_t type_size(int32_t t) { return t == MOK_TYPE_BF16 ? 2 : 4; }
 constexpr int32_t kMaxRouteTokens = (1 << 26) - 4;
 constexpr int32_t kMaxBiasLayers = (1 << 22) - 1;
 
+// A launch has fewer than 2^32 threads; the block products' largest workgroup
+// has 512.  Their operands' rows stay below what 256 of them can be apart in 32 bits.
+constexpr int64_t kMaxWorkgroups = (1ll << 32) / 512 - 1;
+constexpr int32_t kBlock8MaxK = 1 << 20, kBlock8MaxSlots = (1 << 24) - 1;
+
+bool block8_width(int32_t w) { return w > 0 && w % 64 == 0; }
+bool experts_ok(const int32_t* offsets, int32_t n_local) {
+  return n_local >= 1 && n_local <= 256 && (offsets || n_local == 1);
+}
+bool muon_sizes_ok(int32_t n, int32_t rows, int32_t cols) {
+  return n >= 0 && n <= kMuonMaxMats && rows >= 1 && rows <= kMuonMaxSide && cols >= 1 && cols <= kMuonMaxSide;
+}
+bool newton_schulz_ok(const mok_newton_schulz* ns) {
+  return ns && ns->steps >= 1 && ns->steps <= 32 && std::isfinite(ns->a) && std::isfinite(ns->b) &&
+         std::isfinite(ns->c);
+}
+
 thread_local hipError_t g_last_hip_error = hipSuccess;
 
 mok_status hip_status(hipError_t e) {
@@ -281,6 +301,131 @@ mok_status mok_route_bias_update(int32_t* load, int32_t n_layers, int32_t E, flo
   if (odd(load, 4) || odd(bias, 4)) return MOK_ERR_INVALID_ARG;
   if (n_layers > kMaxBiasLayers) return MOK_ERR_UNSUPPORTED;
   return hip_status(launch_bias_update(load, n_layers, E, rate, bias, clear_load != 0, stream));
+}
+
+int64_t mok_block8_slots(int32_t rows, int32_t n_local) {
+  return rows < 0 || n_local < 1 || n_local > 256 ? 0 : block8_slots(rows, n_local);
+}
+
+mok_status mok_block8_quantise(const mok_block8_source* src, int32_t rows, int32_t W,
+                               const int32_t* offsets, int32_t n_local, uint8_t* codes,
+                               float* scales, uint8_t* codes_t, float* scales_t, int32_t t_scales,
+                               hipStream_t stream) {
+  if (!src || rows < 0 || !block8_width(W) || !experts_ok(offsets, n_local)) return MOK_ERR_INVALID_ARG;
+  if (src->op < MOK_BLOCK8_COPY || src->op > MOK_BLOCK8_SWIGLU_BWD || !type_ok(src->type) ||
+      src->reserved != 0 || src->ring_rows < 0 ||
+      (t_scales != MOK_BLOCK8_LINES && t_scales != MOK_BLOCK8_BLOCKS))
+    return MOK_ERR_INVALID_ARG;
+  if (!codes != !scales || !codes_t != !scales_t || (!codes && !codes_t)) return MOK_ERR_INVALID_ARG;
+  const bool bwd = src->op == MOK_BLOCK8_SWIGLU_BWD;
+  const size_t size = type_size(src->type);
+  if (src->ring_rows) {
+    if (src->op != MOK_BLOCK8_COPY || src->type != MOK_TYPE_BF16) return MOK_ERR_INVALID_ARG;
+  } else if (src->ld < (src->op == MOK_BLOCK8_SWIGLU ? 2 * static_cast<int64_t>(W) : W) ||
+             (bwd && src->ldd < W / 2)) {
+    return MOK_ERR_INVALID_ARG;
+  }
+  if (rows > 0 && (!src->x || (bwd && !src->d))) return MOK_ERR_INVALID_ARG;
+  if (odd(src->x, size) || odd(src->d, size) || odd(offsets, 4) || odd(codes, 16) || odd(scales, 4) ||
+      odd(codes_t, 16) || odd(scales_t, 4))
+    return MOK_ERR_INVALID_ARG;
+  const int64_t tiles = block8_slots(rows, n_local) / kBlock * ((W + kBlock - 1) / kBlock);
+  if (tiles > kMaxWorkgroups) return MOK_ERR_UNSUPPORTED;
+  return hip_status(launch_block8_quantise(*src, rows, W, offsets, n_local, codes, scales, codes_t,
+                                           scales_t, t_scales == MOK_BLOCK8_BLOCKS, stream));
+}
+
+mok_status mok_block8_quantise_weights(const void* w, int32_t type, int32_t n, int32_t N, int32_t K,
+                                       uint8_t* codes, float* scales, uint8_t* codes_t,
+                                       float* scales_t, hipStream_t stream) {
+  if (!type_ok(type) || n < 0 || !block8_width(N) || !block8_width(K)) return MOK_ERR_INVALID_ARG;
+  if ((n > 0 && (!w || !codes || !scales)) || !codes_t != !scales_t) return MOK_ERR_INVALID_ARG;
+  if (odd(w, type_size(type)) || odd(codes, 16) || odd(scales, 4) || odd(codes_t, 16) || odd(scales_t, 4))
+    return MOK_ERR_INVALID_ARG;
+  const int64_t tiles = static_cast<int64_t>((N + kBlock - 1) / kBlock) * ((K + kBlock - 1) / kBlock);
+  if (n > 65535 || tiles * n > kMaxWorkgroups) return MOK_ERR_UNSUPPORTED;
+  return hip_status(launch_block8_weights(w, type == MOK_TYPE_BF16, n, N, K, codes, scales, codes_t,
+                                          scales_t, stream));
+}
+
+mok_status mok_block8_gemm(const uint8_t* a, const float* a_scales, int32_t rows, int32_t K,
+                           const int32_t* offsets, int32_t n_local, const uint8_t* w,
+                           const float* w_scales, int32_t N, void* out, int32_t out_type,
+                           hipStream_t stream) {
+  if (rows < 0 || !block8_width(K) || !block8_width(N) || !experts_ok(offsets, n_local) || !type_ok(out_type))
+    return MOK_ERR_INVALID_ARG;
+  if (rows > 0 && (!a || !a_scales || !w || !w_scales || !out)) return MOK_ERR_INVALID_ARG;
+  if (odd(a, 16) || odd(a_scales, 4) || odd(offsets, 4) || odd(w, 16) || odd(w_scales, 4) || odd(out, 16))
+    return MOK_ERR_INVALID_ARG;
+  if (K > kBlock8MaxK || static_cast<int64_t>(N) * K >= 1ll << 32 ||
+      block8_slots(rows, n_local) / 16 * ((N + 63) / 64) > kMaxWorkgroups)
+    return MOK_ERR_UNSUPPORTED;
+  Block8Product p{};
+  p.t = a; p.t_scales = a_scales; p.w = w; p.w_scales = w_scales;
+  p.offsets = offsets; p.n_local = n_local; p.rows = rows; p.K = K; p.N = N;
+  p.out = out; p.bf16 = out_type == MOK_TYPE_BF16;
+  return hip_status(launch_block8_gemm(p, stream));
+}
+
+mok_status mok_block8_wgrad(const uint8_t* dy_t, const float* dy_scales, int32_t M,
+                            const uint8_t* x_t, const float* x_scales, int32_t N, int32_t rows,
+                            const int32_t* offsets, int32_t n_local, void* dw, int32_t out_type,
+                            int32_t accumulate, hipStream_t stream) {
+  if (rows < 0 || !block8_width(M) || !block8_width(N) || !experts_ok(offsets, n_local) || !type_ok(out_type) ||
+      (accumulate != 0 && (accumulate != 1 || out_type != MOK_TYPE_F32)))
+    return MOK_ERR_INVALID_ARG;
+  if (!dw || (rows > 0 && (!dy_t || !dy_scales || !x_t || !x_scales))) return MOK_ERR_INVALID_ARG;
+  if (odd(dy_t, 16) || odd(dy_scales, 4) || odd(x_t, 16) || odd(x_scales, 4) || odd(offsets, 4) || odd(dw, 16))
+    return MOK_ERR_INVALID_ARG;
+  const int64_t S = block8_slots(rows, n_local);
+  if (S > kBlock8MaxSlots || static_cast<int64_t>(n_local) * ((M + 63) / 64) * ((N + 63) / 64) > kMaxWorkgroups)
+    return MOK_ERR_UNSUPPORTED;
+  Block8Product p{};
+  p.t = dy_t; p.t_scales = dy_scales; p.w = x_t; p.w_scales = x_scales;
+  p.offsets = offsets; p.n_local = n_local; p.rows = rows; p.M = M; p.N = N;
+  p.S = static_cast<int32_t>(S);
+  p.out = dw; p.bf16 = out_type == MOK_TYPE_BF16; p.accumulate = accumulate;
+  return hip_status(launch_block8_wgrad(p, stream));
+}
+
+size_t mok_muon_workspace_size(int32_t n, int32_t rows, int32_t cols) {
+  return muon_sizes_ok(n, rows, cols) ? muon_ws_bytes(n, rows, cols) : 0;
+}
+
+mok_status mok_orthogonalise(const void* x, int32_t type, int32_t n, int32_t rows, int32_t cols,
+                             const mok_newton_schulz* ns, void* out, void* ws, size_t ws_bytes,
+                             hipStream_t stream) {
+  if (!type_ok(type) || !muon_sizes_ok(n, rows, cols) || !newton_schulz_ok(ns)) return MOK_ERR_INVALID_ARG;
+  if (n > 0 && (!x || !out || !ws)) return MOK_ERR_INVALID_ARG;
+  if (odd(x, type_size(type)) || odd(out, 2) || odd(ws, 256)) return MOK_ERR_INVALID_ARG;
+  if (n > 0 && ws_bytes < muon_ws_bytes(n, rows, cols)) return MOK_ERR_WORKSPACE;
+  MuonArgs a{};
+  a.x = x; a.x_bf16 = type == MOK_TYPE_BF16; a.out = out;
+  a.n = n; a.rows = rows; a.cols = cols; a.ns = *ns; a.ws = ws;
+  return hip_status(launch_muon(a, stream));
+}
+
+mok_status mok_muon_step(float* p, void* p_bf16, const void* grad, int32_t grad_type, float* m,
+                         int32_t n, int32_t rows, int32_t cols, const mok_muon_hyper* hyper,
+                         const mok_adamw_scalars* scalars, void* ws, size_t ws_bytes,
+                         hipStream_t stream) {
+  if (!type_ok(grad_type) || !muon_sizes_ok(n, rows, cols) || !hyper || !newton_schulz_ok(&hyper->ns))
+    return MOK_ERR_INVALID_ARG;
+  const mok_muon_hyper& h = *hyper;
+  if (!std::isfinite(h.lr) || !(h.momentum >= 0.0 && h.momentum < 1.0) || !std::isfinite(h.weight_decay) ||
+      !std::isfinite(h.grad_scale) || !std::isfinite(h.scale) || (h.nesterov != 0 && h.nesterov != 1) ||
+      h.reserved != 0)
+    return MOK_ERR_INVALID_ARG;
+  if (n > 0 && (!p || !grad || !m || !ws)) return MOK_ERR_INVALID_ARG;
+  if (odd(p, 4) || odd(p_bf16, 2) || odd(grad, type_size(grad_type)) || odd(m, 4) || odd(scalars, 16) || odd(ws, 256))
+    return MOK_ERR_INVALID_ARG;
+  if (n > 0 && ws_bytes < muon_ws_bytes(n, rows, cols)) return MOK_ERR_WORKSPACE;
+  MuonArgs a{};
+  a.x = grad; a.x_bf16 = grad_type == MOK_TYPE_BF16; a.p = p; a.p_bf16 = p_bf16; a.m = m;
+  a.n = n; a.rows = rows; a.cols = cols; a.ns = h.ns; a.ws = ws;
+  a.lr = h.lr; a.momentum = h.momentum; a.weight_decay = h.weight_decay;
+  a.grad_scale = h.grad_scale; a.scale = h.scale; a.nesterov = h.nesterov; a.scalars = scalars;
+  return hip_status(launch_muon(a, stream));
 }
 
 size_t mok_adamw_table_size(int32_t n_tensors) {

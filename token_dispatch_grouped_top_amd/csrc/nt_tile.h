@@ -1,0 +1,93 @@
+// nt_tile.h -- tile loop of products of two operands whose rows lie along the
+// contraction (both "row-major, K contiguous"): the 8-bit block products and
+// the fp16 products of the orthogonalised update.  A K-step is 128 bytes of a
+// row (128 E4M3 codes or 64 fp16 values): one cache line of HBM, 8 chunks of
+// 16 bytes in LDS.
+//
+// Roles: D[i][j] = sum_k W[i][k] T[j][k] with W the MFMA's first operand, so a
+// lane holds, for one row j of T, runs of four consecutive i.  An output whose
+// rows are j has i as its contiguous direction.
+//
+// Loads go straight to LDS (buffer loads with 16 bytes a lane, NS stages); a
+// row or chunk outside an operand reads as zero through the buffer's extent.
+// Chunk c of row r lies at place c ^ key(r), which a lane realises by what it
+// asks for, since the direct load puts lanes behind each other.
+#pragma once
+
+#include "mok_internal.h"
+
+namespace mok {
+namespace nt {
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(1))) const void* glb_ptr_t;
+
+constexpr int kRow = 128;                      // bytes of a row in a stage
+constexpr uint32_t kOutside = 0xfffffff0u;     // a buffer offset past every extent
+
+// Place of logical chunk c of row r: eight rows behind each other hold one
+// chunk at eight different places, and the next eight rows at the other four
+// of each pair, so a fragment's 16-byte reads spread over the banks.
+__device__ __forceinline__ int chunk_at(int r, int c) { return c ^ ((r & 7) ^ ((r >> 3) & 1)); }
+
+template <int N> __device__ __forceinline__ void wait_vm_barrier() {
+  static_assert(N >= 0 && N <= 63, "vmcnt range");
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// TT x TW: rows of T and of W in a workgroup's tile; WT x WW waves; NS stages.
+// SCALES: 4-byte slots for scales in each stage.
+template <int TT_, int TW_, int WT_, int WW_, int NS_, bool SCALES_> struct Geo {
+  static constexpr int TT = TT_, TW = TW_, WT = WT_, WW = WW_, NS = NS_;
+  static constexpr bool SCALES = SCALES_;
+  static constexpr int WAVES = WT * WW, THREADS = 64 * WAVES;
+  static constexpr int FT = TT / WT / 32, FW = TW / WW / 32;       // 32-row fragments of a wave
+  static constexpr int LT = TT * kRow / 1024 / WAVES, LW = TW * kRow / 1024 / WAVES;   // loads of a wave
+  static constexpr int LPS = LT + LW + (SCALES ? 1 : 0);
+  static constexpr int STAGE = (TT + TW) * kRow + (SCALES ? THREADS * 4 : 0);
+  static constexpr int EPI = WAVES * 32 * (32 * FW + 4) * 4;       // a wave's 32 rows of fp32 results
+  static constexpr int LDS = NS * STAGE > EPI ? NS * STAGE : EPI;
+  static_assert(FT >= 1 && FW >= 1 && LT >= 1 && LW >= 1, "every wave loads and multiplies");
+  static_assert(!SCALES || TT + TW / 128 + 1 <= THREADS, "a thread for each scale");
+  static_assert(LDS <= 160 * 1024, "LDS budget");
+};
+
+// One operand of a tile: `base` at the tile's first row and first K-step.
+struct Operand {
+  const uint8_t* base;
+  int64_t stride;              // bytes between rows
+  int64_t extent;              // bytes from base on that may be read
+};
+
+template <int L> struct Loader {
+  __amdgpu_buffer_rsrc_t rsrc;
+  uint32_t at[L], tail[L];     // offsets at step 0; at a step that is only half there
+  // `rows` rows of the tile exist; wave `wave` of `waves` loads KiB j * waves + wave.
+  __device__ __forceinline__ Loader(const Operand& o, int rows, int wave, int waves, int lane) {
+    const int64_t e = o.extent < 0xfffffff0ll ? o.extent : 0xfffffff0ll;
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.base), 0, static_cast<int32_t>(e),
+                                             0x00020000);
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      const int r = (j * waves + wave) * 8 + lane / 8, c = chunk_at(r, lane % 8);
+      at[j] = r < rows ? static_cast<uint32_t>(r * o.stride + c * 16) : kOutside;
+      tail[j] = c < 4 ? at[j] : kOutside;
+    }
+  }
+};
+
+// LDS address of a fragment chunk: rows 32 f + lane % 32 of a wave's block,
+// whose first row is a multiple of 32; the place of a chunk depends on the
+// lane alone.
+__device__ __forceinline__ u32x4_t chunk16(const uint8_t* p) {
+  return *reinterpret_cast<const u32x4_t*>(p);
+}
+
+}  // namespace nt
+}  // namespace mok
