@@ -176,3 +176,21 @@ def test_muon_scalars():
     numbers.view(torch.int32)[3] = 1
     a = step(numbers)
     assert torch.equal(a[0], dev(p0, torch.float32)) and torch.equal(a[1], dev(m0))
+
+
+@pytest.mark.parametrize("n,rows,cols", [(40, 256, 256), (20, 320, 300), (1, 384, 4160), (3, 1100, 900), (100, 40, 70)])
+def test_repeats_are_equal(n, rows, cols):
+    """The same call gives the same bits: with several workgroups on a CU, with K in pieces, in every tile size."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn(n, rows, cols, generator=gen, device="cuda")
+    ws, first = workspace(n, rows, cols), None
+    for _ in range(6):
+        out = torch.empty(n, rows, cols, dtype=torch.bfloat16, device="cuda")
+        mok.mok_orthogonalise(x, n, rows, cols, out, ws)
+        first = out if first is None else first
+        assert torch.equal(out, first)
+    y = x[n // 2].double() / x[n // 2].double().norm()
+    for _ in range(5):
+        g = y @ y.T.contiguous()
+        y = COEF[0] * y + (COEF[1] * g + COEF[2] * g @ g) @ y
+    assert (first[n // 2].double() - y).norm() <= 2.0 ** -7 * y.norm()

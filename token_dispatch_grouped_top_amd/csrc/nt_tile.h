@@ -41,6 +41,21 @@ template <int N> __device__ __forceinline__ void wait_vm_barrier() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// Asks the scheduler to put one of A LDS reads behind each of the first of M
+// matrix instructions, and B loads from memory evenly behind the others.  (Reads
+// come first in the program, too: a load to LDS does not pass a read.)
+template <int M, int A, int B, int m = 0> __device__ __forceinline__ void interleave() {
+  if constexpr (m < M) {
+    constexpr int per = A >= M ? (A + M - 1) / M : 1, from = A >= M ? M - 1 : A;
+    constexpr int reads = m * per < A ? (A - m * per < per ? A - m * per : per) : 0;
+    constexpr int loads = m < from ? 0 : B * (m + 1 - from) / (M - from) - B * (m - from) / (M - from);
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+    interleave<M, A, B, m + 1>();
+  }
+}
+
 // TT x TW: rows of T and of W in a workgroup's tile; WT x WW waves; NS stages.
 // SCALES: 4-byte slots for scales in each stage.
 template <int TT_, int TW_, int WT_, int WW_, int NS_, bool SCALES_> struct Geo {
