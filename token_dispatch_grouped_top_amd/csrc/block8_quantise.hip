@@ -3,10 +3,17 @@
 // transposed into slot blocks, and of weight matrices.
 //
 // scale = max(amax / 448, 2^-126), code = RNE(fl(value / scale)).  One
-// workgroup takes 128 rows x 128 columns, reads them once into registers (8 x 8
+// workgroup takes 128 rows x 128 columns, reads them once into registers (4 x 8
 // values a thread) and forms every scale that the tile has: of its rows, of
 // its columns, of the whole.  The transposed codes go through LDS, so that both
-// outputs are written in whole lines.  Bound: bytes.
+// outputs are written in whole lines.  Bound: bytes, as long as a value costs
+// few instructions (8192 x 7168 bf16 both ways: 55 us, 4.3 TB/s; with a test for
+// NaN and IEEE divisions at each value it was 114): magnitudes are compared as
+// whole numbers, in pairs where they are bf16, which shows what is not finite
+// for nothing; a quotient is a product and one correction; and what is not
+// finite then becomes NaN by itself.  Four rows a thread need 40 to 80 registers;
+// eight need 64 to 150 and gain nothing (55 us; SwiGLU of 4095 x 2048 17.4 us
+// instead of 16.3).
 #include <algorithm>
 
 #include "block8.h"
@@ -58,43 +65,88 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, float (&v)[8
   }
 }
 
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
+// Eight values of a row in registers: as bf16 pairs where they come as such
+// (half the registers, twice the waves), else in fp32.
+template <bool PAIRS> struct Row8;
+template <> struct Row8<true> {
+  uint32_t w[4];
+  __device__ __forceinline__ void set(uint4 u) { w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w; }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0; }
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+};
+template <> struct Row8<false> {
+  float v[8];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  }
+  __device__ __forceinline__ float operator[](int i) const { return v[i]; }
+};
+
+// Magnitudes are compared as whole numbers, the values' bits without their
+// sign: in that order infinity and NaN lie above every finite value, so a
+// largest one says whether a block has any.
+constexpr uint32_t kInf = 0x7f800000u;
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_pairs(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
 
 // Largest of the 16 lanes of a DPP row, in all of them.
-__device__ __forceinline__ float max16(float m) {
-#define MOK_ROT(n)                                                                                  \
-  m = fmaxf(m, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(m), 0x120 + (n), 0xf, \
-                                                           0xf, true)))
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+#define MOK_ROT(n) m = umax(m, __builtin_amdgcn_update_dpp(0, m, 0x120 + (n), 0xf, 0xf, true))
   MOK_ROT(8); MOK_ROT(4); MOK_ROT(2); MOK_ROT(1);
 #undef MOK_ROT
   return m;
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return fmaxf(amax / 448.0f, 0x1p-126f); }
-
-// x / s rounded as fp32 division rounds it: a quotient from the reciprocal r
-// of s (itself rounded correctly) and one correction, which would lose the
-// sign of a zero.
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float q = x * r;
-  return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, x), r, q), x);
-}
-// What is converted: at most 448 in magnitude, NaN (of which the conversion makes 0xff) for a value that is not finite.
-__device__ __forceinline__ float to_code(float x, float s, float r) {
-  return finite(x) ? __builtin_amdgcn_fmed3f(quotient(x, s, r), -448.0f, 448.0f) : __builtin_nanf("");
-}
+// A block's scale s and 1 / s from its largest magnitude.  amax / 448 as fp32
+// division rounds it: from the rounded reciprocal of 448 and one correction
+// (scales below 2^-126 are not used).
+struct Scale {
+  float s, r;
+  Scale() = default;
+  __device__ __forceinline__ explicit Scale(uint32_t amax) {
+    const float a = __uint_as_float(amax), q = a * (1.0f / 448.0f);
+    s = fmaxf(__builtin_fmaf(__builtin_fmaf(-q, 448.0f, a), 1.0f / 448.0f, q), 0x1p-126f);
+    r = __builtin_amdgcn_rcpf(s);
+    r = __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
+  }
+  // x / s as fp32 division rounds it, from the reciprocal and one correction
+  // (subtracted in this way it leaves a zero its sign).  At most 448 + 2^-15,
+  // which converts to 448.
+  __device__ __forceinline__ float operator()(float x) const {
+    const float q = x * r;
+    return __builtin_fmaf(-__builtin_fmaf(q, s, -x), r, q);
+  }
+};
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
 }
 
+// e^-x for x >= 0, off by the rounding of x log2 e and a last place; the
+// instruction gives zero for what is subnormal, so that is formed 2^64 larger.
+__device__ __forceinline__ float exp_minus(float x) {
+  const float t = x * -1.44269504f;
+  const bool small = t < -126.0f;
+  return __builtin_amdgcn_exp2f(small ? t + 64.0f : t) * (small ? 0x1p-64f : 1.0f);
+}
+
+constexpr int RP = 4, THREADS = 16 * kBlock / RP, WAVES = THREADS / kWave;   // rows of a thread
 // grid: (column blocks x row blocks, matrices)
 template <int OP, int MODE, bool BF16, bool VEC>
-__global__ __launch_bounds__(256) void k_block8_quantise(const QuantArgs a) {
-  constexpr bool T = MODE != ROWS;
+__global__ __launch_bounds__(THREADS) void k_block8_quantise(const QuantArgs a) {
+  constexpr bool T = MODE != ROWS, PAIRS = OP == MOK_BLOCK8_COPY && BF16 && VEC;
   constexpr int PITCH = 128 + 8;
   __shared__ __attribute__((aligned(16))) uint8_t tile[T ? 128 * PITCH : 16];
-  __shared__ float s_max[4][128];
+  __shared__ uint32_t s_max[MODE == LINES ? WAVES : 1][128];
+  __shared__ float2 s_scale[MODE == LINES ? 128 : 1];
+  __shared__ uint32_t s_all[WAVES];
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
   const int c8 = tid & 15, rg = tid >> 4;
   const int cb = blockIdx.x % a.col_blocks, rb = blockIdx.x / a.col_blocks;
@@ -128,21 +180,21 @@ __global__ __launch_bounds__(256) void k_block8_quantise(const QuantArgs a) {
   }
   const int64_t mat = MODE == WEIGHTS ? static_cast<int64_t>(blockIdx.y) * a.rows * a.W : 0;
 
-  // ---- values: rows 8 rg .. 8 rg + 7, columns 8 c8 .. 8 c8 + 7
-  float v[8][8];
+  // ---- values: rows RP rg .. RP rg + RP - 1, columns 8 c8 .. 8 c8 + 7
+  Row8<PAIRS> v[RP];
   const int half = a.W / 2;                     // MOK_BLOCK8_SWIGLU_BWD: I
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int r = 8 * rg + p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[p][i] = 0.0f;
+  for (int p = 0; p < RP; ++p) {
+    const int r = RP * rg + p;
+    v[p].clear();
     if (r >= nrows || col >= a.W) continue;
     const int64_t row = row0 + r;
     if constexpr (OP == MOK_BLOCK8_COPY) {
-      if (MODE != WEIGHTS && a.ring_rows)
-        load8<BF16, VEC>(a.x, colblk_byte(row % a.ring_rows, a.ring_rows, 2 * col) / 2, v[p]);
-      else
-        load8<BF16, VEC>(a.x, mat + row * a.ld + col, v[p]);
+      const int64_t at = MODE != WEIGHTS && a.ring_rows
+                             ? colblk_byte(row % a.ring_rows, a.ring_rows, 2 * col) / 2
+                             : mat + row * a.ld + col;
+      if constexpr (PAIRS) v[p].set(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + at));
+      else load8<BF16, VEC>(a.x, at, v[p].v);
     } else {
       const int I = OP == MOK_BLOCK8_SWIGLU ? a.W : half;
       const bool up = OP == MOK_BLOCK8_SWIGLU_BWD && col >= I;   // the du half
@@ -154,91 +206,147 @@ __global__ __launch_bounds__(256) void k_block8_quantise(const QuantArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // s and 1 - s from e^-|g|, which does not overflow: both keep their digits down to the subnormal
-        const float e = expf(-fabsf(g[i])), near1 = 1.0f / (1.0f + e), near0 = e * near1;
+        const float e = exp_minus(fabsf(g[i])), one = 1.0f + e;
+        float near1 = __builtin_amdgcn_rcpf(one);
+        near1 = __builtin_fmaf(__builtin_fmaf(-one, near1, 1.0f), near1, near1);
+        const float near0 = e * near1;
         const float s = g[i] < 0.0f ? near0 : near1, t = g[i] < 0.0f ? near1 : near0;
-        if (OP == MOK_BLOCK8_SWIGLU) v[p][i] = g[i] * s * u[i];
-        else v[p][i] = up ? d[i] * g[i] * s : d[i] * u[i] * s * (1.0f + g[i] * t);
+        if (OP == MOK_BLOCK8_SWIGLU) v[p].v[i] = g[i] * s * u[i];
+        else v[p].v[i] = up ? d[i] * g[i] * s : d[i] * u[i] * s * (1.0f + g[i] * t);
       }
     }
   }
 
-  // ---- scales of the rows, and their codes
-  float row_max[8], col_max[8];
+  // ---- largest magnitudes of the thread's rows and columns, of the tile (and
+  // of its columns, in LDS).  If one is not finite they are formed once more
+  // without such values.
+  uint32_t row_max[RP], all = 0;
+  auto maxima = [&](bool finite) {
+    uint32_t col_max[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) col_max[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) col_max[i] = 0;
+    if (PAIRS && finite) {
+      if constexpr (PAIRS) {
+        uint32_t cm[4] = {0, 0, 0, 0};
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    float m = 0.0f;
+        for (int p = 0; p < RP; ++p) {
+          uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = finite(v[p][i]) ? fabsf(v[p][i]) : 0.0f;
-      m = fmaxf(m, x);
-      col_max[i] = fmaxf(col_max[i], x);
+          for (int i = 0; i < 4; ++i) {
+            w[i] = v[p].w[i] & 0x7fff7fffu;
+            cm[i] = max_pairs(cm[i], w[i]);
+          }
+          const uint32_t m = max_pairs(max_pairs(w[0], w[1]), max_pairs(w[2], w[3]));
+          row_max[p] = umax(m << 16, m & 0xffff0000u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          col_max[2 * i] = cm[i] << 16;
+          col_max[2 * i + 1] = cm[i] & 0xffff0000u;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int p = 0; p < RP; ++p) {
+        row_max[p] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x = v[p][i];
+          if (!finite) asm volatile("" : "+v"(x));   // not kept from the first time: 64 registers
+          uint32_t m = magnitude(x);
+          if (!finite && m >= kInf) m = 0;
+          row_max[p] = umax(row_max[p], m);
+          col_max[i] = umax(col_max[i], m);
+        }
+      }
     }
-    row_max[p] = m;
-  }
-  float block_scale = 0.0f, col_scale[8];
-  if constexpr (T) {
+    all = 0;
+#pragma unroll
+    for (int p = 0; p < RP; ++p) all = umax(all, row_max[p]);
+    all = max16(all);
+    all = umax(all, __shfl_xor(all, 16));
+    all = umax(all, __shfl_xor(all, 32));
+    if (lane == 0) s_all[wave] = all;
     if constexpr (MODE == LINES) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        col_max[i] = fmaxf(col_max[i], __shfl_xor(col_max[i], 16));
-        col_max[i] = fmaxf(col_max[i], __shfl_xor(col_max[i], 32));
-        if (lane < 16) s_max[wave][8 * c8 + i] = col_max[i];
+        uint32_t m = umax(col_max[i], __shfl_xor(col_max[i], 16));
+        m = umax(m, __shfl_xor(m, 32));
+        if (lane < 16) s_max[wave][8 * c8 + i] = m;
       }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = 8 * c8 + i;
-        col_scale[i] = scale_of(fmaxf(fmaxf(s_max[0][c], s_max[1][c]), fmaxf(s_max[2][c], s_max[3][c])));
-      }
-    } else {
-      float m = row_max[0];
-#pragma unroll
-      for (int p = 1; p < 8; ++p) m = fmaxf(m, row_max[p]);
-      m = max16(m);
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      if (lane == 0) s_max[wave][0] = m;
-      __syncthreads();
-      block_scale = scale_of(fmaxf(fmaxf(s_max[0][0], s_max[1][0]), fmaxf(s_max[2][0], s_max[3][0])));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) col_scale[i] = block_scale;
     }
+    __syncthreads();
+    all = s_all[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) all = umax(all, s_all[w]);
+  };
+  maxima(true);
+  if (__builtin_expect(all >= kInf, 0)) {
+    __syncthreads();
+    maxima(false);
   }
+  // What is converted: NaN (of which the conversion makes 0xff) for a value that
+  // is not finite: of infinity the correction makes it.
+  auto quotient = [&](const Scale& s, int p, int i) { return s(v[p][i]); };
+
+  // ---- the rows' codes
+  const Scale whole(MODE == BLOCKS || MODE == WEIGHTS ? all : 0);
   if (MODE == WEIGHTS || a.codes) {
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-      const float s = MODE == WEIGHTS ? block_scale : scale_of(max16(row_max[p]));
-      const float r = 1.0f / s;
-      const int row = 8 * rg + p;
+    for (int p = 0; p < RP; ++p) {
+      const Scale s = MODE == WEIGHTS ? whole : Scale(max16(row_max[p]));
+      const int row = RP * rg + p;
       if (row < nrows && col < a.W) {
         uint2 w;
-        w.x = pack4(to_code(v[p][0], s, r), to_code(v[p][1], s, r), to_code(v[p][2], s, r), to_code(v[p][3], s, r));
-        w.y = pack4(to_code(v[p][4], s, r), to_code(v[p][5], s, r), to_code(v[p][6], s, r), to_code(v[p][7], s, r));
+        w.x = pack4(quotient(s, p, 0), quotient(s, p, 1), quotient(s, p, 2), quotient(s, p, 3));
+        w.y = pack4(quotient(s, p, 4), quotient(s, p, 5), quotient(s, p, 6), quotient(s, p, 7));
         *reinterpret_cast<uint2*>(a.codes + mat + (row0 + row) * a.W + col) = w;
-        if (MODE != WEIGHTS && c8 == 0) a.scales[static_cast<int64_t>(cb) * a.rows + row0 + row] = s;
+        if (MODE != WEIGHTS && c8 == 0) a.scales[static_cast<int64_t>(cb) * a.rows + row0 + row] = s.s;
       }
+      if (PAIRS) __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   // ---- the transposed codes
   if constexpr (T) {
+    if constexpr (PAIRS) {                      // not unpacked twice over: 64 registers
+#pragma unroll
+      for (int p = 0; p < RP; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(v[p].w[i]));
+    }
+    __builtin_amdgcn_sched_barrier(0);
     if (MODE != WEIGHTS || a.codes_t) {
+      if constexpr (MODE == LINES) {            // a column's scale once, for all of its threads
+        if (tid < kBlock) {
+          uint32_t m = s_max[0][tid];
+#pragma unroll
+          for (int w = 1; w < WAVES; ++w) m = umax(m, s_max[w][tid]);
+          const Scale s(m);
+          s_scale[tid] = make_float2(s.s, s.r);
+          if (cb * kBlock + tid < a.W) a.scales_t[static_cast<int64_t>(rb) * a.W + cb * kBlock + tid] = s.s;
+        }
+        __syncthreads();
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = col_scale[i], r = 1.0f / s;
-        uint2 w;
-        w.x = pack4(to_code(v[0][i], s, r), to_code(v[1][i], s, r), to_code(v[2][i], s, r), to_code(v[3][i], s, r));
-        w.y = pack4(to_code(v[4][i], s, r), to_code(v[5][i], s, r), to_code(v[6][i], s, r), to_code(v[7][i], s, r));
-        *reinterpret_cast<uint2*>(tile + (8 * c8 + i) * PITCH + 8 * rg) = w;
+        const int c = 8 * c8 + i;
+        Scale s = whole;
+        if constexpr (MODE == LINES) {
+          const float2 x = s_scale[c];
+          s.s = x.x;
+          s.r = x.y;
+        }
+        *reinterpret_cast<uint32_t*>(tile + c * PITCH + RP * rg) =
+            pack4(quotient(s, 0, i), quotient(s, 1, i), quotient(s, 2, i), quotient(s, 3, i));
+        __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
       // columns of the tile: 8 lanes and 16 bytes each; a matrix's last block of rows may be half one
       const int64_t place = MODE == WEIGHTS ? row0 : static_cast<int64_t>(rb) * kBlock;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int c = 32 * k + tid / 8, at = tid % 8 * 16;
+      for (int k = 0; k < 128 * 8 / THREADS; ++k) {
+        const int c = THREADS / 8 * k + tid / 8, at = tid % 8 * 16;
         if (cb * kBlock + c < a.W && (MODE != WEIGHTS || at < nrows)) {
           const uint2 lo = *reinterpret_cast<const uint2*>(tile + c * PITCH + at);
           const uint2 hi = *reinterpret_cast<const uint2*>(tile + c * PITCH + at + 8);
@@ -247,19 +355,13 @@ __global__ __launch_bounds__(256) void k_block8_quantise(const QuantArgs a) {
         }
       }
     }
-    const int64_t col_blocks = a.col_blocks;
-    if (MODE == LINES) {
-      if (tid < 16 && col < a.W) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a.scales_t[static_cast<int64_t>(rb) * a.W + col + i] = col_scale[i];
-      }
-    } else if (tid == 0) {
+    if (MODE != LINES && tid == 0) {
       if (MODE == BLOCKS) {
-        a.scales_t[cb * (a.S / kBlock) + rb] = block_scale;
+        a.scales_t[cb * (a.S / kBlock) + rb] = whole.s;
       } else {
-        const int64_t row_blocks = (a.rows + kBlock - 1) / kBlock, each = row_blocks * col_blocks;
-        a.scales[blockIdx.y * each + rb * col_blocks + cb] = block_scale;
-        if (a.codes_t) a.scales_t[blockIdx.y * each + cb * row_blocks + rb] = block_scale;
+        const int64_t col_blocks = a.col_blocks, row_blocks = (a.rows + kBlock - 1) / kBlock, each = row_blocks * col_blocks;
+        a.scales[blockIdx.y * each + rb * col_blocks + cb] = whole.s;
+        if (a.codes_t) a.scales_t[blockIdx.y * each + cb * row_blocks + rb] = whole.s;
       }
     }
   }
@@ -267,8 +369,8 @@ __global__ __launch_bounds__(256) void k_block8_quantise(const QuantArgs a) {
 
 template <int OP, int MODE, bool BF16>
 hipError_t run(const QuantArgs& a, bool vec, dim3 grid, hipStream_t s) {
-  if (vec) hipLaunchKernelGGL((k_block8_quantise<OP, MODE, BF16, true>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((k_block8_quantise<OP, MODE, BF16, false>), grid, dim3(256), 0, s, a);
+  if (vec) hipLaunchKernelGGL((k_block8_quantise<OP, MODE, BF16, true>), grid, dim3(THREADS), 0, s, a);
+  else hipLaunchKernelGGL((k_block8_quantise<OP, MODE, BF16, false>), grid, dim3(THREADS), 0, s, a);
   return hipGetLastError();
 }
 template <int OP, int MODE> hipError_t run(const QuantArgs& a, bool bf16, bool vec, dim3 grid, hipStream_t s) {
