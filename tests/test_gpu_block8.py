@@ -336,3 +336,44 @@ def test_wgrad(counts, M, N, out):
                 size = size + ref.wgrad(dy, sdy, x, sx, counts, drop=True)[1] * 2.0 ** 23 / (max(counts) + 131)
             tol = (max(counts) + 131) * 2.0 ** -23 * size + (2.0 ** -8 if out == "bf16" else 2.0 ** -24) * np.abs(want)
             assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.parametrize("counts,K,N", [([2300], 320, 1280), ([1100, 0, 300, 900], 384, 2368), ([260, 100, 520], 192, 512),
+                                        ([257] * 8, 256, 1088)])
+def test_gemm_tiles(counts, K, N):
+    """Sizes whose tiles fill the CUs once and a part: whole tiles, tiles cut in two and four, tiles of few rows; every
+    result is exact, and the same when computed again."""
+    rng = np.random.default_rng(N)
+    rows, n = sum(counts), len(counts)
+    a, w = small_codes(rng, rows, K), small_codes(rng, n, N, K)
+    sa = np.exp2(rng.integers(-2, 3, (ref.blocks(K), rows))).astype(np.float32)
+    sw = np.exp2(rng.integers(-2, 3, (n, ref.blocks(N), ref.blocks(K)))).astype(np.float32)
+    want, size = ref.product(a, sa, counts, w, sw)
+    assert size.max() * 16 < 2 ** 24
+    args = [dev(a), dev(sa), rows, K, dev(w), dev(sw), N]
+    for out in (torch.bfloat16, torch.float32):
+        for _ in range(3):
+            y = torch.full((rows, N), -7.0, dtype=out, device="cuda")
+            mok.mok_block8_gemm(*args, y, offsets=offsets_of(counts), n_local=n)
+            assert torch.equal(y, torch.from_numpy(want).to(out).cuda())
+
+
+@pytest.mark.parametrize("counts,M,N", [([1500], 512, 1344), ([600, 700, 0, 800], 320, 768), ([300] * 20, 512, 576)])
+def test_wgrad_tiles(counts, M, N):
+    rng = np.random.default_rng(N)
+    rows, n = sum(counts), len(counts)
+    S = ref.slots(rows, n)
+    used = np.zeros(S, np.uint8)
+    for c, at in zip(counts, ref.starts(counts)):
+        used[at:at + c] = 1
+    dy, x = small_codes(rng, M, S) * used, small_codes(rng, N, S) * used
+    sdy = np.exp2(rng.integers(-2, 3, (S // 128, M))).astype(np.float32)
+    sx = np.exp2(rng.integers(-2, 3, (ref.blocks(N), S // 128))).astype(np.float32)
+    want, size = ref.wgrad(dy, sdy, x, sx, counts)
+    assert size.max() * 16 < 2 ** 24
+    args = [dev(dy), dev(sdy), M, dev(x), dev(sx), N, rows]
+    for out in (torch.bfloat16, torch.float32):
+        for _ in range(3):
+            dw = torch.full((n, M, N), -7.0, dtype=out, device="cuda")
+            mok.mok_block8_wgrad(*args, dw, offsets=offsets_of(counts), n_local=n)
+            assert torch.equal(dw, torch.from_numpy(want).to(out).cuda())

@@ -363,7 +363,7 @@ mok_status mok_block8_gemm(const uint8_t* a, const float* a_scales, int32_t rows
   Block8Product p{};
   p.t = a; p.t_scales = a_scales; p.w = w; p.w_scales = w_scales;
   p.offsets = offsets; p.n_local = n_local; p.rows = rows; p.K = K; p.N = N;
-  p.out = out; p.bf16 = out_type == MOK_TYPE_BF16;
+  p.out = out; p.bf16 = out_type == MOK_TYPE_BF16; p.n_cus = device_cus();
   return hip_status(launch_block8_gemm(p, stream));
 }
 
@@ -385,6 +385,7 @@ mok_status mok_block8_wgrad(const uint8_t* dy_t, const float* dy_scales, int32_t
   p.offsets = offsets; p.n_local = n_local; p.rows = rows; p.M = M; p.N = N;
   p.S = static_cast<int32_t>(S);
   p.out = dw; p.bf16 = out_type == MOK_TYPE_BF16; p.accumulate = accumulate;
+  p.n_cus = device_cus();
   return hip_status(launch_block8_wgrad(p, stream));
 }
 

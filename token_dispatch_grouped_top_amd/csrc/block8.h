@@ -31,6 +31,7 @@ struct Block8Product {
   int32_t S;                                   // gradient: places of the operands' rows
   void* out;
   int32_t bf16, accumulate;
+  int32_t n_cus;                               // of the device
 };
 hipError_t launch_block8_gemm(const Block8Product& p, hipStream_t s);
 hipError_t launch_block8_wgrad(const Block8Product& p, hipStream_t s);
@@ -92,7 +93,7 @@ struct ExpertRows {
         blocks += 4 * lane + j < e ? (count[j] + kBlock - 1) / kBlock : 0;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) blocks += __shfl_xor(blocks, d);
-      *slots = static_cast<int64_t>(kBlock) * blocks;
+      *slots = static_cast<int64_t>(kBlock) * __builtin_amdgcn_readfirstlane(blocks);
     }
     return true;
   }

@@ -22,6 +22,8 @@
 //
 // The gradient of the weights is the same product over slot blocks: dy_t takes
 // the tokens' place (a scale for 128 slots of a column), x_t the weights'.
+#include <type_traits>
+
 #include "block8.h"
 #include "nt_tile.h"
 
@@ -111,32 +113,20 @@ __device__ __forceinline__ void block8_step(f32x16_t (&acc)[G::FW][G::FT], const
   }
 }
 
-template <class G, bool WGRAD, bool EXACT>
-__device__ __forceinline__ void block8_tile(const Block8Product& p, int n_wt, uint8_t* __restrict__ lds) {
-  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+// What a workgroup computes: the G::TT x G::TW results of expert e from row t0
+// (of its t_all) and column i0 on.
+struct Job {
+  int e, t0, i0, t_all;
+  int32_t row0, count;         // the expert's rows
+  int64_t slots;               // its first place
+};
 
-  // ---- which tile: expert by expert, columns outside, rows inside, each XCD
-  // a contiguous eighth of them (workgroup ids go round the XCDs)
-  const ExpertRows ex(p.offsets, p.n_local, p.rows, lane);
-  int units[4], total = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    units[i] = WGRAD ? (4 * lane + i < p.n_local ? (p.M + G::TT - 1) / G::TT * n_wt : 0)
-                     : (ex.count[i] + G::TT - 1) / G::TT * n_wt;
-    total += units[i];
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
-  total = __builtin_amdgcn_readfirstlane(total);
-  const int q = total / 8, rest = total % 8, x = blockIdx.x % 8, at = blockIdx.x / 8;
-  if (at >= q + (x < rest)) return;
-  const int t = x * q + (x < rest ? x : rest) + at;
-  int e, before;
-  int32_t row0, count;
-  int64_t slots = 0;
-  if (!ex.find(units, t, lane, e, before, row0, count, WGRAD ? &slots : nullptr)) return;
-  const int t_all = WGRAD ? p.M : count, t_tiles = (t_all + G::TT - 1) / G::TT;
-  const int t0 = (t - before) % t_tiles * G::TT, i0 = (t - before) / t_tiles * G::TW;
+template <class G, bool WGRAD, bool EXACT>
+__device__ __forceinline__ void block8_tile(const Block8Product& p, const Job& job, uint8_t* __restrict__ lds) {
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int e = job.e, t0 = job.t0, i0 = job.i0, t_all = job.t_all;
+  const int32_t row0 = job.row0, count = job.count;
+  const int64_t slots = job.slots;
 
   // ---- operands
   const int t_rows = t_all - t0 < G::TT ? t_all - t0 : G::TT;
@@ -166,37 +156,43 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, int n_wt, ui
     ws = p.w_scales + (static_cast<int64_t>(e) * ((p.N + kBlock - 1) / kBlock) + i0 / kBlock) * steps;
   }
   const int64_t ws_row = WGRAD ? p.S / kBlock : steps;
-  const Loader<G::LT> lt(ot, t_rows, wave, G::WAVES, lane);
-  const Loader<G::LW> lw(ow, w_rows, wave, G::WAVES, lane);
-  // a thread's scale: of row tid of the tokens, or of one of the tile's blocks of weight rows
-  const float* my_scale;
-  int64_t my_step;
-  if (tid < G::TT) {
-    my_scale = ts + (tid < t_rows ? tid : t_rows - 1);
-    my_step = ts_step;
-  } else {
-    int b = tid - G::TT;
-    const int blocks = (w_rows + kBlock - 1) / kBlock;
-    my_scale = ws + (b < blocks ? b : blocks - 1) * ws_row;
-    my_step = 1;
-  }
-  auto stage_t = [&](int b) { return lds + b * G::STAGE; };
-  auto stage_w = [&](int b) { return lds + b * G::STAGE + G::TT * kRow; };
-  auto stage_s = [&](int b) { return lds + b * G::STAGE + (G::TT + G::TW) * kRow; };
-  auto issue = [&](int step, int b) {
-    step = step < steps ? step : steps - 1;                // past the end: loads that nobody reads
+  const Loader<G::WAVES> lt(ot, wave, lane), lw(ow, wave, lane);
+  // A thread's scale of a step: of row tid of the tokens; of one of the tile's
+  // blocks of weight rows from the first wave behind those on.
+  static_assert(G::TT % 64 == 0, "a wave's scales are of one kind");
+  const bool t_wave = wave < G::TT / 64;
+  const int blocks = (w_rows + kBlock - 1) / kBlock;
+  const float* scale_at = t_wave ? ts : ws;                // advanced by the steps' number times
+  const int64_t scale_step = t_wave ? ts_step : 1;
+  const uint32_t my_scale = t_wave ? (tid < t_rows ? tid : t_rows - 1) * 4u
+                                   : static_cast<uint32_t>((lane < blocks ? lane : blocks - 1) * ws_row * 4);
+  // (all stages of an operand behind each other: 64 KiB, what an offset in an instruction reaches)
+  auto stage_t = [&](int b) { return lds + b * (G::TT * kRow); };
+  auto stage_w = [&](int b) { return lds + G::NS * G::TT * kRow + b * (G::TW * kRow); };
+  auto stage_s = [&](int b) { return lds + G::NS * (G::TT + G::TW) * kRow + b * (G::THREADS * 4); };
+  // A stage's loads: tokens and scales, or weights.  Past the last step they are
+  // of the last one, and nobody reads them.
+  auto issue_t = [&](int step, int b) {
+    step = step < steps ? step : steps - 1;
     const bool cut = half && step == steps - 1;
-    const uint32_t off = static_cast<uint32_t>(step) * kRow;
-#pragma unroll
-    for (int j = 0; j < G::LT; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(lt.rsrc, (lds_ptr_t)(stage_t(b) + (j * G::WAVES + wave) * 1024),
-                                               16, cut ? lt.tail[j] : lt.at[j], off, 0, 0);
-#pragma unroll
-    for (int j = 0; j < G::LW; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(lw.rsrc, (lds_ptr_t)(stage_w(b) + (j * G::WAVES + wave) * 1024),
-                                               16, cut ? lw.tail[j] : lw.at[j], off, 0, 0);
-    __builtin_amdgcn_global_load_lds((glb_ptr_t)(my_scale + step * my_step),
-                                     (lds_ptr_t)(stage_s(b) + wave * 256), 4, 0, 0);
+    static_assert(G::LT <= 4 && G::LW <= 8, "loads of a stage");
+    lt.template load<0>(stage_t(b), wave, step, cut);
+    if constexpr (G::LT > 1) lt.template load<1>(stage_t(b), wave, step, cut);
+    if constexpr (G::LT > 2) { lt.template load<2>(stage_t(b), wave, step, cut); lt.template load<3>(stage_t(b), wave, step, cut); }
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(scale_at + step * scale_step), 0, 0x7fffffff, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr_t)(stage_s(b) + wave * 256), 4, my_scale, 0, 0, 0);
+  };
+  auto issue_w = [&](int step, int b) {
+    step = step < steps ? step : steps - 1;
+    const bool cut = half && step == steps - 1;
+    lw.template load<0>(stage_w(b), wave, step, cut);
+    if constexpr (G::LW > 1) lw.template load<1>(stage_w(b), wave, step, cut);
+    if constexpr (G::LW > 2) { lw.template load<2>(stage_w(b), wave, step, cut); lw.template load<3>(stage_w(b), wave, step, cut); }
+    if constexpr (G::LW > 4) {
+      lw.template load<4>(stage_w(b), wave, step, cut); lw.template load<5>(stage_w(b), wave, step, cut);
+      lw.template load<6>(stage_w(b), wave, step, cut); lw.template load<7>(stage_w(b), wave, step, cut);
+    }
   };
 
   // ---- main loop
@@ -208,28 +204,154 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, int n_wt, ui
     for (int j = 0; j < G::FT; ++j)
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
-  if (steps > 0) {
+  if constexpr (!EXACT && G::FW == 2 && G::NS == 2) {
+    if (steps > 0) {
+      // Two stages, one block of 32 x 32 after another.  Of a step's eight blocks
+      // the last one's operands are in registers when the others are done: behind
+      // it stands the barrier that says that this stage is read and the next one
+      // has landed, and while it is multiplied the next step's first operands are
+      // read.  (A burst of reads at the start of a step, by all waves at once, left
+      // the matrix units idle for as long as it took.)  The blocks go up and down
+      // so that the half of the weights' fragments that the next step begins with
+      // is the one that is free first; that is the other one in every second step
+      // (with one row group the same in all of them).
+      // The fma of a block stand behind the matrix instructions of the next.
+      i32x8_t wf[2][2], tf[2][2];
+      f32x16_t part[2];
+      float f[G::FT], last = 0.0f;
 #pragma unroll
-    for (int s = 0; s < G::NS - 1; ++s) issue(s, s);
-  }
-  int buf = 0;
-  for (int s = 0; s < steps; ++s) {
-    wait_vm_barrier<(G::NS - 2) * G::LPS>();
-    issue(s + G::NS - 1, buf == 0 ? G::NS - 1 : buf - 1);
-    const float* sc = reinterpret_cast<const float*>(stage_s(buf));
-    block8_step<G, EXACT>(acc, stage_t(buf) + wt * kRow, stage_w(buf) + ww * kRow, sc + wt,
-                          sc[G::TT + ww / kBlock], lane);
-    buf = buf + 1 == G::NS ? 0 : buf + 1;
+      for (int k = 0; k < 16; ++k) part[1][k] = 0.0f;
+      // A lane's first chunk of the first row group; the other three of a row lie at
+      // that address with bits 5 and 6 turned over.  They are formed where they
+      // are read: kept, they would be a dozen registers of 256.
+      typedef const __attribute__((address_space(3))) u32x4_t* lds_chunk_t;
+      typedef const __attribute__((address_space(3))) float* lds_float_t;
+      const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_ptr_t)lds));
+      const uint32_t t_at = lds0 + (wt + (lane & 31)) * kRow + chunk_at(lane & 31, lane >> 5) * 16;
+      const uint32_t w_off = G::NS * G::TT * kRow + (ww - wt) * kRow;       // from there to the weights' first
+      const uint32_t s_at = lds0 + G::NS * (G::TT + G::TW) * kRow + (wt + (lane & 31)) * 4;
+      const uint32_t s_w = lds0 + G::NS * (G::TT + G::TW) * kRow + (G::TT + ww / kBlock) * 4;
+      auto rows_at = [](uint32_t at, i32x8_t (&to)[2]) {
+        u32x4_t c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<lds_chunk_t>(static_cast<uintptr_t>(at ^ (32u * k)));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          to[h] = __builtin_bit_cast(i32x8_t, __builtin_shufflevector(c[2 * h], c[2 * h + 1], 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      static_assert(G::FT == 1 || G::FT % 2 == 0, "how the blocks of a step end");
+      constexpr bool ONE = G::FT == 1;                     // one row group: its fragments change places with every step
+      auto read_t = [&](int b, int j, int slot) {
+        uint32_t at = t_at, sc = s_at, sw = s_w;
+        asm volatile("" : "+v"(at), "+v"(sc), "+s"(sw));
+        rows_at(at + (b * G::TT + 32 * j) * kRow, tf[slot]);
+        return *reinterpret_cast<lds_float_t>(static_cast<uintptr_t>(sc + b * G::THREADS * 4 + 128 * j)) *
+               *reinterpret_cast<lds_float_t>(static_cast<uintptr_t>(sw + b * G::THREADS * 4));
+      };
+      auto read_w = [&](int b, int i) {
+        uint32_t at = t_at;
+        asm volatile("" : "+v"(at));
+        rows_at(at + w_off + (b * G::TW + 32 * i) * kRow, wf[i]);
+      };
+      auto step = [&](int s, auto parity) {
+        constexpr int P = decltype(parity)::value, B = 2 * G::FT;
+        constexpr int FIRST = ONE ? 0 : P, THEN = ONE ? 0 : 1 - P;   // the halves that this step and the next begin with
+        const auto column = [](int k) { return ((k + 1) / 2 + FIRST) & 1; };
+        float f0 = f[0];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+          const int i = column(k), j = k / 2;
+          if (k == B - 1) {
+            wait_vm_barrier<0>();
+            read_w(1 - P, THEN);
+            f[0] = read_t(1 - P, 0, ONE ? 1 - P : 0);
+            issue_t(s + 2, P);
+          }
+          if (k == 0) {
+            read_w(P, 1 - FIRST);
+            issue_w(s + 1, 1 - P);
+          }
+          if (k % 2 == 1 && k < B - 1) f[j + 1] = read_t(P, j + 1, (j + 1) & 1);
+          const int slot = ONE ? P : j & 1;
+          f32x16_t& p = part[k & 1];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) p[q] = 0.0f;
+          p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i][0], tf[slot][0], p, 0, 0, 0, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i][1], tf[slot][1], p, 0, 0, 0, 0, 0, 0);
+          const int ii = k == 0 ? 1 - FIRST : column(k - 1), jj = k == 0 ? G::FT - 1 : (k - 1) / 2;
+          const float factor = k == 0 ? last : jj == 0 ? f0 : f[jj];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[ii][jj][q] = __builtin_fmaf(part[1 - (k & 1)][q], factor, acc[ii][jj][q]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        last = ONE ? f0 : f[G::FT - 1];
+      };
+      issue_t(0, 0);
+      issue_w(0, 0);
+      issue_t(1, 1);
+      wait_vm_barrier<G::LT + 1>();
+      read_w(0, 0);
+      f[0] = read_t(0, 0, 0);
+      int s = 0;
+      for (; s + 1 < steps; s += 2) {
+        step(s, std::integral_constant<int, 0>());
+        step(s + 1, std::integral_constant<int, 1>());
+      }
+      if (s < steps) step(s, std::integral_constant<int, 0>());
+      if (!ONE && s < steps) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[0][G::FT - 1][q] = __builtin_fmaf(part[1][q], last, acc[0][G::FT - 1][q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[1][G::FT - 1][q] = __builtin_fmaf(part[1][q], last, acc[1][G::FT - 1][q]);
+      }
+    }
+  } else {
+    if (steps > 0) {
+#pragma unroll
+      for (int s = 0; s < G::NS - 1; ++s) {
+        issue_t(s, s);
+        issue_w(s, s);
+      }
+    }
+    int buf = 0;
+    for (int s = 0; s < steps; ++s) {
+      wait_vm_barrier<(G::NS - 2) * G::LPS>();
+      const int to = buf == 0 ? G::NS - 1 : buf - 1;
+      issue_t(s + G::NS - 1, to);
+      issue_w(s + G::NS - 1, to);
+      const float* sc = reinterpret_cast<const float*>(stage_s(buf));
+      block8_step<G, EXACT>(acc, stage_t(buf) + wt * kRow, stage_w(buf) + ww * kRow, sc + wt, sc[G::TT + ww / kBlock], lane);
+      buf = buf + 1 == G::NS ? 0 : buf + 1;
+    }
   }
   wait_vm_barrier<0>();
 
   // ---- results: 32 rows at a time through the wave's own part of LDS, so that
-  // a row's columns are stored behind each other
-  constexpr int CW = 32 * G::FW, PITCH = CW + 4, LPR = CW / 4;   // lanes of a row
+  // a row's columns are stored behind each other.  What they are added to is
+  // loaded a group ahead: a load does not pass the stores.
+  constexpr int CW = 32 * G::FW, PITCH = CW + 4, LPR = CW / 4, NK = 32 * LPR / 64;   // LPR: lanes of a row
   float* own = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
   const int64_t out0 = WGRAD ? static_cast<int64_t>(e) * p.M + t0 : static_cast<int64_t>(row0) + t0;
+  const bool add = WGRAD && EXACT && p.accumulate;
+  float4 old[2][NK];
+  auto place = [&](int j, int k, int64_t& o) {
+    const int tr = wt + 32 * j + (k * 64 + lane) / LPR, col = i0 + ww + (k * 64 + lane) % LPR * 4;
+    o = (out0 + tr) * p.N + col;
+    return tr < t_rows && col < p.N && col < i0 + G::TW;
+  };
+  auto fetch = [&](int j) {
+    if constexpr (WGRAD && EXACT) {
+      int64_t o;
+#pragma unroll
+      for (int k = 0; k < NK; ++k)
+        if (add && place(j, k, o)) old[j & 1][k] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.out) + o);
+    }
+  };
+  fetch(0);
 #pragma unroll
   for (int j = 0; j < G::FT; ++j) {
+    if (j + 1 < G::FT) fetch(j + 1);
 #pragma unroll
     for (int i = 0; i < G::FW; ++i)
 #pragma unroll
@@ -237,35 +359,85 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, int n_wt, ui
         *reinterpret_cast<float4*>(own + (lane & 31) * PITCH + 32 * i + 8 * g + 4 * (lane >> 5)) =
             make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
 #pragma unroll
-    for (int k = 0; k < 32 * LPR / 64; ++k) {
-      const int r = (k * 64 + lane) / LPR, c = (k * 64 + lane) % LPR * 4;
-      float4 v = *reinterpret_cast<const float4*>(own + r * PITCH + c);
-      const int tr = wt + 32 * j + r, col = i0 + ww + c;
-      if (tr < t_rows && col < p.N) {
-        const int64_t o = (out0 + tr) * p.N + col;
-        if constexpr (!EXACT) {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
-              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-        } else {
-          float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.out) + o);
-          if (p.accumulate) {
-            const float4 w = *to;
-            v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
-          }
-          *to = v;
+    for (int k = 0; k < NK; ++k) {
+      float4 v = *reinterpret_cast<const float4*>(own + (k * 64 + lane) / LPR * PITCH + (k * 64 + lane) % LPR * 4);
+      int64_t o;
+      if (!place(j, k, o)) continue;
+      if constexpr (!EXACT) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + o) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+      } else {
+        if (add) {
+          const float4 w = old[j & 1][k];
+          v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
         }
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = v;
       }
     }
   }
 }
 
-template <class G, bool WGRAD, bool EXACT>
-__global__ __launch_bounds__(G::THREADS) void k_block8(const Block8Product p, int n_wt) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[G::LDS];
-  block8_tile<G, WGRAD, EXACT>(p, n_wt, lds);
+// Workgroup -> tile: expert by expert, columns outside, rows inside, each XCD a
+// contiguous eighth of them (workgroup ids go round the XCDs).  The tiles that
+// would make a last round of their own, with most of the XCD's CUs idle, are
+// cut into two or four by columns where there are CUs for that (SPLIT); a tile
+// with few rows is one of half the rows.
+template <class G, bool WGRAD, bool EXACT, bool SPLIT>
+__device__ __forceinline__ void block8_job(const Block8Product& p, int n_wt, uint8_t* __restrict__ lds) {
+  const int lane = lane_id();
+  const ExpertRows ex(p.offsets, p.n_local, p.rows, lane);
+  int units[4], total = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    units[i] = WGRAD ? (4 * lane + i < p.n_local ? (p.M + G::TT - 1) / G::TT * n_wt : 0)
+                     : (ex.count[i] + G::TT - 1) / G::TT * n_wt;
+    total += units[i];
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  total = __builtin_amdgcn_readfirstlane(total);
+  const int q = total / 8, rest = total % 8, x = blockIdx.x % 8, c = q + (x < rest);
+  int at = blockIdx.x / 8, piece = 0, pieces = 1;
+  if constexpr (SPLIT) {
+    const int P = p.n_cus / 8, last = P > 0 ? c % P : 0;
+    pieces = last == 0 ? 1 : 4 * last <= P ? 4 : 2 * last <= P ? 2 : 1;
+    if (at >= c - last) {
+      const int u = at - (c - last);
+      piece = u % pieces;
+      at = c - last + u / pieces;
+    } else {
+      pieces = 1;
+    }
+  }
+  if (at >= c) return;
+  const int t = x * q + (x < rest ? x : rest) + at;
+  Job job;
+  int before;
+  job.slots = 0;
+  if (!ex.find(units, t, lane, job.e, before, job.row0, job.count, WGRAD ? &job.slots : nullptr)) return;
+  job.t_all = WGRAD ? p.M : job.count;
+  const int t_tiles = (job.t_all + G::TT - 1) / G::TT;
+  job.t0 = (t - before) % t_tiles * G::TT;
+  job.i0 = (t - before) / t_tiles * G::TW;
+  if constexpr (SPLIT) {
+    static_assert(G::TT == 256 && G::TW == 256 && G::WAVES == 8, "the parts of this tile");
+    job.i0 += piece * (G::TW / pieces);
+    if (job.i0 >= p.N) return;
+    if (pieces == 4) return block8_tile<Geo<256, 64, 8, 1, 2, true>, WGRAD, EXACT>(p, job, lds);
+    if (pieces == 2) return block8_tile<Geo<256, 128, 4, 2, 2, true>, WGRAD, EXACT>(p, job, lds);
+    if (job.t_all - job.t0 <= 128) return block8_tile<Geo<128, 256, 2, 4, 2, true>, WGRAD, EXACT>(p, job, lds);
+  }
+  block8_tile<G, WGRAD, EXACT>(p, job, lds);
 }
 
-template <class G, bool WGRAD> hipError_t run(const Block8Product& p, hipStream_t s) {
+template <class G, bool WGRAD, bool EXACT, bool SPLIT>
+__global__ __launch_bounds__(G::THREADS) void k_block8(const Block8Product p, int n_wt) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[G::LDS];
+  block8_job<G, WGRAD, EXACT, SPLIT>(p, n_wt, lds);
+}
+
+template <class G, bool WGRAD, bool EXACT> hipError_t run(const Block8Product& p, hipStream_t s) {
+  constexpr bool SPLIT = G::TT == 256 && G::TW == 256;
   const int64_t n_wt = (p.N + G::TW - 1) / G::TW;
   int64_t tt;
   if (WGRAD) {
@@ -274,24 +446,30 @@ template <class G, bool WGRAD> hipError_t run(const Block8Product& p, hipStream_
     tt = (static_cast<int64_t>(p.rows) + G::TT - 1) / G::TT + p.n_local - 1;
     if (tt > p.rows) tt = p.rows;
   }
-  if (tt * n_wt == 0) return hipSuccess;
-  const dim3 grid(static_cast<unsigned>(tt * n_wt));
-  if (p.bf16) hipLaunchKernelGGL((k_block8<G, WGRAD, false>), grid, dim3(G::THREADS), 0, s, p, static_cast<int>(n_wt));
-  else hipLaunchKernelGGL((k_block8<G, WGRAD, true>), grid, dim3(G::THREADS), 0, s, p, static_cast<int>(n_wt));
+  if (tt == 0) return hipSuccess;
+  // an XCD's pieces are at most as many as its CUs
+  const int64_t grid = tt * n_wt + (SPLIT ? p.n_cus : 0);
+  hipLaunchKernelGGL((k_block8<G, WGRAD, EXACT, SPLIT>), dim3(static_cast<unsigned>(grid)), dim3(G::THREADS), 0, s, p,
+                     static_cast<int>(n_wt));
   return hipGetLastError();
 }
 
 using Big = Geo<256, 256, 2, 4, 2, true>;
+using Wide = Geo<128, 256, 2, 4, 2, true>;     // fp16's products of the same: half the accumulators
 using Mid = Geo<64, 128, 1, 4, 3, true>;
+using Out = Geo<128, 128, 2, 2, 2, true>;      // gradients of few slots: two to a CU, stores under other tiles' loads
 
 }  // namespace
 
 hipError_t launch_block8_gemm(const Block8Product& p, hipStream_t s) {
-  return p.rows / p.n_local >= 128 ? run<Big, false>(p, s) : run<Mid, false>(p, s);
+  if (p.rows / p.n_local >= 128) return p.bf16 ? run<Big, false, false>(p, s) : run<Wide, false, true>(p, s);
+  return p.bf16 ? run<Mid, false, false>(p, s) : run<Mid, false, true>(p, s);
 }
 
 hipError_t launch_block8_wgrad(const Block8Product& p, hipStream_t s) {
-  return p.M >= 256 && p.N >= 256 ? run<Big, true>(p, s) : run<Mid, true>(p, s);
+  if (p.rows / p.n_local < 256 || p.M < 256 || p.N < 256)
+    return p.bf16 ? run<Out, true, false>(p, s) : run<Out, true, true>(p, s);
+  return p.bf16 ? run<Big, true, false>(p, s) : run<Wide, true, true>(p, s);
 }
 
 }  // namespace mok

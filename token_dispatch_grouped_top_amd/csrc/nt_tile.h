@@ -80,20 +80,29 @@ struct Operand {
   int64_t extent;              // bytes from base on that may be read
 };
 
-template <int L> struct Loader {
+// Loads of an operand's rows, eight rows (1 KiB) an instruction: wave `wave` of
+// WAVES takes KiB j * WAVES + wave of a stage.  A lane's row and chunk in the
+// first of its KiB are one offset; the others lie whole rows further on (the
+// chunk's place is the same: WAVES is even).  Rows past the operand's last lie
+// past its extent.
+template <int WAVES> struct Loader {
+  static_assert(WAVES % 2 == 0, "a lane's chunk is the same in all of its KiB");
   __amdgpu_buffer_rsrc_t rsrc;
-  uint32_t at[L], tail[L];     // offsets at step 0; at a step that is only half there
-  // `rows` rows of the tile exist; wave `wave` of `waves` loads KiB j * waves + wave.
-  __device__ __forceinline__ Loader(const Operand& o, int rows, int wave, int waves, int lane) {
+  uint32_t at;                 // offset of step 0
+  uint32_t next;               // bytes to the next KiB's rows
+  bool far;                    // a chunk that a half step does not have
+  __device__ __forceinline__ Loader(const Operand& o, int wave, int lane) {
     const int64_t e = o.extent < 0xfffffff0ll ? o.extent : 0xfffffff0ll;
     rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.base), 0, static_cast<int32_t>(e),
                                              0x00020000);
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-      const int r = (j * waves + wave) * 8 + lane / 8, c = chunk_at(r, lane % 8);
-      at[j] = r < rows ? static_cast<uint32_t>(r * o.stride + c * 16) : kOutside;
-      tail[j] = c < 4 ? at[j] : kOutside;
-    }
+    const int r = wave * 8 + lane / 8, c = chunk_at(r, lane % 8);
+    at = static_cast<uint32_t>(r * o.stride + c * 16);
+    far = c >= 4;
+    next = static_cast<uint32_t>(WAVES * 8 * o.stride);
+  }
+  template <int J> __device__ __forceinline__ void load(uint8_t* stage, int wave, uint32_t step, bool half) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(stage + (J * WAVES + wave) * 1024), 16, half && far ? kOutside : at,
+                                             step * kRow + J * next, 0, 0);
   }
 };
 
