@@ -454,22 +454,155 @@ template <class G, bool WGRAD, bool EXACT> hipError_t run(const Block8Product& p
   return hipGetLastError();
 }
 
+// A 32 x 32 tile whose waves each take every eighth block of K, from registers:
+// for products of few tiles, which wait in every step of a loop that all waves
+// run together (for its barrier, the reads behind it, two matrix instructions
+// and what they are added to: 0.55 us, however far ahead the loads go).  The
+// waves' sums are added in their order.
+constexpr int kThin = 32, kThinWaves = 8;
+template <bool EXACT>
+__device__ __forceinline__ void block8_thin(const Block8Product& p, uint8_t* __restrict__ lds) {
+  const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int r = lane & 31, h = lane >> 5;
+  const int n_wt = (p.N + kThin - 1) / kThin;
+  const ExpertRows ex(p.offsets, p.n_local, p.rows, lane);
+  int units[4], e, before;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) units[i] = (ex.count[i] + kThin - 1) / kThin * n_wt;
+  int32_t row0, count;
+  if (!ex.find(units, blockIdx.x, lane, e, before, row0, count)) return;
+  const int t_tiles = (count + kThin - 1) / kThin, at = blockIdx.x - before;
+  const int t0 = at % t_tiles * kThin, i0 = at / t_tiles * kThin;
+  const int t_rows = count - t0 < kThin ? count - t0 : kThin, w_rows = p.N - i0 < kThin ? p.N - i0 : kThin;
+  const int steps = (p.K + kBlock - 1) / kBlock;
+  auto rsrc = [&](const uint8_t* base, int rows) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, rows * p.K, 0x00020000);   // below 2^26
+  };
+  const __amdgpu_buffer_rsrc_t rt = rsrc(p.t + (static_cast<int64_t>(row0) + t0) * p.K, t_rows);
+  const __amdgpu_buffer_rsrc_t rw = rsrc(p.w + (static_cast<int64_t>(e) * p.N + i0) * p.K, w_rows);
+  const float* ts = p.t_scales + row0 + t0 + (r < t_rows ? r : t_rows - 1);
+  const float* ws = p.w_scales + (static_cast<int64_t>(e) * ((p.N + kBlock - 1) / kBlock) + i0 / kBlock) * steps;
+  const int row_at = r * p.K;
+  struct Step { u32x4_t t[4], w[4]; float f; };
+  // chunks h, 2 + h, 4 + h, 6 + h of the lane's rows; what a half block does not have reads as zero
+  auto load = [&](int s, Step& x) {
+    if (s >= steps) return;
+    const bool cut = p.K % kBlock != 0 && s == steps - 1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int off = cut && k >= 2 ? 0x7ffffff0 : row_at + (2 * k + h) * 16;
+      x.t[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rt, off, s * kBlock, 0));
+      x.w[k] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, off, s * kBlock, 0));
+    }
+    x.f = ts[static_cast<int64_t>(s) * p.rows] * ws[s];
+  };
+  f32x16_t acc;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) acc[k] = 0.0f;
+  auto add = [&](const Step& x) {
+    f32x16_t part;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) part[k] = 0.0f;
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          part = __builtin_amdgcn_mfma_f32_32x32x16_f16(to_f16(x.w[k], g), to_f16(x.t[k], g), part, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        part = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            __builtin_bit_cast(i32x8_t, __builtin_shufflevector(x.w[2 * k], x.w[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7)),
+            __builtin_bit_cast(i32x8_t, __builtin_shufflevector(x.t[2 * k], x.t[2 * k + 1], 0, 1, 2, 3, 4, 5, 6, 7)),
+            part, 0, 0, 0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] = __builtin_fmaf(part[k], x.f, acc[k]);
+  };
+  Step a, b;
+  load(wave, a);
+  for (int s = wave; s < steps; s += 2 * kThinWaves) {
+    load(s + kThinWaves, b);
+    add(a);
+    if (s + kThinWaves >= steps) break;
+    load(s + 2 * kThinWaves, a);
+    add(b);
+  }
+  constexpr int PITCH = kThin + 4;
+  float* own = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<float4*>(own + (wave * kThin + r) * PITCH + 8 * g + 4 * h) =
+        make_float4(acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]);
+  __syncthreads();
+  const int tr = tid / 16, c = tid % 16 * 2;
+  float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < kThinWaves; ++w) {
+    const float2 x = *reinterpret_cast<const float2*>(own + (w * kThin + tr) * PITCH + c);
+    v.x += x.x;
+    v.y += x.y;
+  }
+  if (tr < t_rows && c < w_rows) {
+    const int64_t o = (static_cast<int64_t>(row0) + t0 + tr) * p.N + i0 + c;
+    if constexpr (EXACT) *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o) = v;
+    else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + o) = pack_bf16x2(v.x, v.y);
+  }
+}
+
+template <bool EXACT>
+__global__ __launch_bounds__(kThinWaves * kWave) void k_block8_thin(const Block8Product p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kThinWaves * kThin * (kThin + 4) * 4];
+  block8_thin<EXACT>(p, lds);
+}
+
+hipError_t run_thin(const Block8Product& p, hipStream_t s) {
+  int64_t tt = (static_cast<int64_t>(p.rows) + kThin - 1) / kThin + p.n_local - 1;
+  if (tt > p.rows) tt = p.rows;
+  if (tt == 0) return hipSuccess;
+  const dim3 grid(static_cast<unsigned>(tt * ((p.N + kThin - 1) / kThin)));
+  if (p.bf16) hipLaunchKernelGGL(k_block8_thin<false>, grid, dim3(kThinWaves * kWave), 0, s, p);
+  else hipLaunchKernelGGL(k_block8_thin<true>, grid, dim3(kThinWaves * kWave), 0, s, p);
+  return hipGetLastError();
+}
+
 using Big = Geo<256, 256, 2, 4, 2, true>;
-using Wide = Geo<128, 256, 2, 4, 2, true>;     // fp16's products of the same: half the accumulators
-using Mid = Geo<64, 128, 1, 4, 3, true>;
-using Out = Geo<128, 128, 2, 2, 2, true>;      // gradients of few slots: two to a CU, stores under other tiles' loads
+using Mid = Geo<64, 128, 1, 4, 3, true>;       // two to a CU
+using Mid16 = Geo<64, 128, 1, 4, 2, true>;     // fp16's products: three to a CU (85 us with two, 76 with three)
+using Out = Geo<128, 128, 2, 2, 2, true>;      // gradients: two to a CU, stores under other tiles' loads
+
+// Tiles of an even split of the rows.
+template <class G> int64_t even_tiles(const Block8Product& p) {
+  const int64_t each = (static_cast<int64_t>(p.rows) + p.n_local - 1) / p.n_local;
+  return (each + G::TT - 1) / G::TT * p.n_local * ((p.N + G::TW - 1) / G::TW);
+}
 
 }  // namespace
 
+// Measured, in us, 256 x 256 tiles against 64 x 128: 8192 rows of 8 experts,
+// 7168 -> 4096 (512 large tiles) 277 / 430; 4096 of 8, 2048 -> 7168 (448) 72 /
+// 108; 4096 of 32, 2048 -> 1408 (192) 26 / 29; 640 of 8, 7168 -> 4096 (128) 64 /
+// 46; 2048 of 16, 2048 -> 1024 (64) 20 / 14.  fp16's products gain nothing from
+// large tiles (151 / 153, 37 / 34).  32 x 32 against 64 x 128: 4 rows, 7168 ->
+// 1408 (44 small tiles) 11 / 30; 512 rows, 7168 -> 512 (256) 17 / 31; 16 rows of
+// 8 experts, 7168 -> 2048 (512) 22 / 32; 256 rows, 2048 -> 2048 (512) 12 / 12;
+// 1024 rows, 4096 -> 1024 (1024) 33 / 20; fp32 results 11 / 42, 18 / 43, 23 / 44,
+// 12 / 16, 34 / 28.
 hipError_t launch_block8_gemm(const Block8Product& p, hipStream_t s) {
-  if (p.rows / p.n_local >= 128) return p.bf16 ? run<Big, false, false>(p, s) : run<Wide, false, true>(p, s);
-  return p.bf16 ? run<Mid, false, false>(p, s) : run<Mid, false, true>(p, s);
+  if (p.bf16 && p.rows / p.n_local >= 128 && even_tiles<Big>(p) >= 160) return run<Big, false, false>(p, s);
+  const int64_t each = (static_cast<int64_t>(p.rows) + p.n_local - 1) / p.n_local;
+  if ((each + kThin - 1) / kThin * p.n_local * ((p.N + kThin - 1) / kThin) <= 2 * p.n_cus) return run_thin(p, s);
+  return p.bf16 ? run<Mid, false, false>(p, s) : run<Mid16, false, true>(p, s);
 }
 
+// Measured: 8192 slots of 8 experts, 7168 x 2048: 210 us; 4096 of 32, 1408 x
+// 2048: 65 / 72; 4096 of one, 1024 x 1024: 23 / 30; with fp32 results the
+// smaller tile is as good or better (93 / 104, 41 / 54).
 hipError_t launch_block8_wgrad(const Block8Product& p, hipStream_t s) {
-  if (p.rows / p.n_local < 256 || p.M < 256 || p.N < 256)
-    return p.bf16 ? run<Out, true, false>(p, s) : run<Out, true, true>(p, s);
-  return p.bf16 ? run<Big, true, false>(p, s) : run<Wide, true, true>(p, s);
+  if (!p.bf16) return run<Out, true, true>(p, s);
+  if (p.rows / p.n_local < 128 || p.M < 256 || p.N < 256) return run<Out, true, false>(p, s);
+  return run<Big, true, false>(p, s);
 }
 
 }  // namespace mok
