@@ -305,3 +305,32 @@ def test_no_rows():
     assert (dw == 3).all()
     mok.mok_block8_wgrad(*args)
     assert not dw.any()
+
+
+def test_overlapping_runs_stay_inside():
+    """Offsets that are no partition: every expert all of the rows.  Results are not defined; what lies behind the outputs
+    stays, and the next call with a partition is right."""
+    R, W = 260, 256
+    bad = torch.tensor([0, R] * E, dtype=torch.int32, device="cuda")[:E + 1].contiguous()
+    good = torch.tensor([R * e // E for e in range(E + 1)], dtype=torch.int32, device="cuda")
+    S = mok.mok_block8_slots(R, E)
+    x = torch.randn(R, W, device="cuda").bfloat16()
+    sizes = dict(codes=R * W, codes_t=W * S)
+    buf = {n: torch.full((v + 4096,), 9, dtype=torch.uint8, device="cuda") for n, v in sizes.items()}
+    scales, scales_t = torch.full((2 * R + 1024,), 9.0, device="cuda"), torch.full((S // 128 * W + 1024,), 9.0, device="cuda")
+    w, sw = u8(E, 128, W), torch.ones(E, 1, 2, device="cuda")
+    y, dw = torch.full((R * 128 + 1024,), 9.0, device="cuda"), torch.full((E * W * W + 1024,), 9.0, device="cuda")
+    tail = lambda: [buf["codes"][sizes["codes"]:], buf["codes_t"][sizes["codes_t"]:], scales[2 * R:],  # noqa: E731
+                    scales_t[S // 128 * W:], y[R * 128:], dw[E * W * W:]]
+    for off in (bad, good):
+        mok.mok_block8_quantise(x, R, W, buf["codes"], scales, codes_t=buf["codes_t"], scales_t=scales_t,
+                                t_scales=LINES, offsets=off, n_local=E)
+        mok.mok_block8_gemm(buf["codes"], scales, R, W, w, sw, 128, y, off, E)
+        mok.mok_block8_wgrad(buf["codes_t"], scales_t, W, buf["codes_t"], torch.ones(2, S // 128, device="cuda"), W, R, dw, off, E)
+        torch.cuda.synchronize()
+        assert all((t == 9).all() for t in tail())
+    counts = (good[1:] - good[:-1]).tolist()
+    want, size = ref.wgrad(host(buf["codes_t"][:W * S].view(W, S)), host(scales_t[:S // 128 * W].view(-1, W)),
+                           host(buf["codes_t"][:W * S].view(W, S)), np.ones((2, S // 128), np.float32), counts)
+    got = host(dw[:E * W * W].view(E, W, W))
+    assert np.all(np.abs(got - want) <= (max(counts) + 130) * 2.0 ** -23 * size + 2.0 ** -24 * np.abs(want))

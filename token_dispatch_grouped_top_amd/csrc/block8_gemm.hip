@@ -415,6 +415,10 @@ __device__ __forceinline__ void block8_job(const Block8Product& p, int n_wt, uin
   int before;
   job.slots = 0;
   if (!ex.find(units, t, lane, job.e, before, job.row0, job.count, WGRAD ? &job.slots : nullptr)) return;
+  if (WGRAD && job.count > p.S - job.slots) {    // runs of rows that overlap: nothing past the operands' places
+    job.count = job.slots < p.S ? static_cast<int32_t>(p.S - job.slots) : 0;
+    job.slots = job.count ? job.slots : 0;
+  }
   job.t_all = WGRAD ? p.M : job.count;
   const int t_tiles = (job.t_all + G::TT - 1) / G::TT;
   job.t0 = (t - before) % t_tiles * G::TT;
@@ -596,9 +600,9 @@ hipError_t launch_block8_gemm(const Block8Product& p, hipStream_t s) {
   return p.bf16 ? run<Mid, false, false>(p, s) : run<Mid16, false, true>(p, s);
 }
 
-// Measured: 8192 slots of 8 experts, 7168 x 2048: 210 us; 4096 of 32, 1408 x
-// 2048: 65 / 72; 4096 of one, 1024 x 1024: 23 / 30; with fp32 results the
-// smaller tile is as good or better (93 / 104, 41 / 54).
+// Measured, in us, 256 x 256 tiles against 128 x 128: 4096 slots of 32 experts,
+// 1408 x 2048: 65 / 72; 4096 of one, 1024 x 1024: 23 / 30; with fp32 results
+// the smaller tile is as good or better (104 / 93, 54 / 41).
 hipError_t launch_block8_wgrad(const Block8Product& p, hipStream_t s) {
   if (!p.bf16) return run<Out, true, true>(p, s);
   if (p.rows / p.n_local < 128 || p.M < 256 || p.N < 256) return run<Out, true, false>(p, s);
