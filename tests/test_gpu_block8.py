@@ -197,8 +197,7 @@ def test_quantise_ring_and_short_offsets():
             assert np.array_equal(got[:end], want[:end]) and (got[end:] == -1).all()
     # rows of a ring begin again at its first row
     out = outputs(rows + 40, W, 1, "line")
-    mok.mok_block8_quantise(blocked, rows + 40, W, *out, offsets=None, ring_rows=ring) if False else \
-        mok.mok_block8_quantise(blocked, rows + 40, W, out[0], out[1], codes_t=out[2], scales_t=out[3], ring_rows=ring)
+    mok.mok_block8_quantise(blocked, rows + 40, W, out[0], out[1], codes_t=out[2], scales_t=out[3], ring_rows=ring)
     assert np.array_equal(host(out[0]), ref.rows_operand(x[np.arange(rows + 40) % ring])[0])
 
 

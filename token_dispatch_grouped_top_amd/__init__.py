@@ -372,20 +372,20 @@ def mok_block8_quantise(x, rows: int, W: int, codes=None, scales=None, source: i
                         offsets=None, n_local: int = 1, ring_rows: int = 0, stream=None) -> None:
     """x (and d): rows of fp32 or bf16, the rows themselves dense; or, with ring_rows, a dense bf16 buffer of
     column-blocked rows.  codes: uint8 or float8_e4m3fn."""
-    device, s = _device(), mok_block8_source(op=source, ring_rows=ring_rows)
+    device, at_d, ldd = _device(), 0, 0
     if ring_rows:
         if not isinstance(x, int) and x is not None and x.dtype is torch.int16:
             x = x.view(torch.bfloat16)
-        s.x, s.type = _buffer(x, "x", _BF16, ring_rows * W, device), MOK_TYPE_BF16
+        at, kind, ld = _buffer(x, "x", _BF16, ring_rows * W, device), MOK_TYPE_BF16, 0
     else:
-        s.x, s.type, s.ld = _rows(x, "x", rows, 2 * W if source == MOK_BLOCK8_SWIGLU else W, device)
+        at, kind, ld = _rows(x, "x", rows, 2 * W if source == MOK_BLOCK8_SWIGLU else W, device)
         if d is not None:
-            s.d, kind, s.ldd = _rows(d, "d", rows, W // 2, device)
-            if kind != s.type:
+            at_d, kind_d, ldd = _rows(d, "d", rows, W // 2, device)
+            if kind_d != kind:
                 raise ValueError(f"d: {d.dtype} where x is {x.dtype}")
-    S = mok_block8_slots(rows, n_local)
+    S = 0 if codes_t is None and scales_t is None else mok_block8_slots(rows, n_local)
     n_scales = S // 128 * W if t_scales == MOK_BLOCK8_LINES else S // 128 * _blocks(W)
-    _check(_lib.mok_block8_quantise(C.byref(s), rows, W,
+    _check(_lib.mok_block8_quantise(mok_block8_source(source, kind, at, ld, at_d, ldd, ring_rows), rows, W,
                                     _buffer(offsets, "offsets", _I32S, n_local + 1, device), n_local,
                                     _buffer(codes, "codes", _CODES, rows * W, device),
                                     _buffer(scales, "scales", _F32, rows * _blocks(W), device),
