@@ -378,7 +378,12 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, const Job& j
 }
 
 // Workgroup -> tile: expert by expert, columns outside, rows inside, each XCD a
-// contiguous eighth of them (workgroup ids go round the XCDs).  The tiles that
+// contiguous eighth of them (workgroup ids go round the XCDs); of gradients an
+// eighth of each expert's, and what eight does not divide in turn, since an
+// expert's tiles are as long as its slots are many (8192 slots of 8 experts, 7168 x
+// 2048: half of them one expert's 210 us, 416 with an eighth of all; uneven by
+// 30 % 192 / 208; even 182 / 182; smaller even ones lose up to a tenth: 4096 of 8,
+// 2048 x 2048 41 / 38).  The tiles that
 // would make a last round of their own, with most of the XCD's CUs idle, are
 // cut into two or four by columns where there are CUs for that (SPLIT); a tile
 // with few rows is one of half the rows.
@@ -396,7 +401,11 @@ __device__ __forceinline__ void block8_job(const Block8Product& p, int n_wt, uin
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
   total = __builtin_amdgcn_readfirstlane(total);
-  const int q = total / 8, rest = total % 8, x = blockIdx.x % 8, c = q + (x < rest);
+  const int q = total / 8, rest = total % 8, x = blockIdx.x % 8;
+  // gradients: tiles of an expert, XCD x's tiles of the first k experts
+  const int n = WGRAD ? (p.M + G::TT - 1) / G::TT * n_wt : 0, left = n % 8;
+  auto upto = [&](int k) { return k * (n / 8) + (k * left + 7 - x) / 8; };
+  const int c = WGRAD ? upto(p.n_local) : q + (x < rest);
   int at = blockIdx.x / 8, piece = 0, pieces = 1;
   if constexpr (SPLIT) {
     const int P = p.n_cus / 8, last = P > 0 ? c % P : 0;
@@ -410,7 +419,14 @@ __device__ __forceinline__ void block8_job(const Block8Product& p, int n_wt, uin
     }
   }
   if (at >= c) return;
-  const int t = x * q + (x < rest ? x : rest) + at;
+  int t = x * q + (x < rest ? x : rest) + at;
+  if constexpr (WGRAD) {
+    int k = 0;                                   // the first expert of four whose tiles reach past `at`
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k += __popcll(__ballot(4 * lane + i < p.n_local && upto(4 * lane + i + 1) <= at));
+    at -= upto(k);
+    t = k * n + (at < n / 8 ? x * (n / 8) + at : n - left + ((x - k * left) & 7));
+  }
   Job job;
   int before;
   job.slots = 0;
