@@ -340,8 +340,7 @@ def test_wgrad(counts, M, N, out):
 @pytest.mark.parametrize("counts,K,N", [([2300], 320, 1280), ([1100, 0, 300, 900], 384, 2368), ([260, 100, 520], 192, 512),
                                         ([257] * 8, 256, 1088)])
 def test_gemm_tiles(counts, K, N):
-    """Sizes whose tiles fill the CUs once and a part: whole tiles, tiles cut in two and four, tiles of few rows; every
-    result is exact, and the same when computed again."""
+    """Sizes of many tiles, the last of an expert with few rows; every result is exact, and the same when computed again."""
     rng = np.random.default_rng(N)
     rows, n = sum(counts), len(counts)
     a, w = small_codes(rng, rows, K), small_codes(rng, n, N, K)
@@ -355,6 +354,27 @@ def test_gemm_tiles(counts, K, N):
             y = torch.full((rows, N), -7.0, dtype=out, device="cuda")
             mok.mok_block8_gemm(*args, y, offsets=offsets_of(counts), n_local=n)
             assert torch.equal(y, torch.from_numpy(want).to(out).cuda())
+
+
+@pytest.mark.parametrize("counts,K,N", [([2300, 0, 1500, 700], 320, 2816), ([300] * 40, 192, 1088), ([257] * 19, 320, 2048),
+                                        ([257] * 22, 256, 1984), ([5000, 1, 0, 130, 900], 128, 2368)])
+def test_gemm_large_tiles(counts, K, N):
+    """Sizes that take the largest tiles (results in bf16): whole ones, the last round's in one, two and four parts, ones
+    of few rows; exact results, and any codes against the bound."""
+    test_gemm_tiles(counts, K, N)
+    rng = np.random.default_rng(K)
+    rows, n = sum(counts), len(counts)
+    a, w = any_codes(rng, rows, K), any_codes(rng, n, N, K)
+    sa = np.exp(rng.normal(size=(ref.blocks(K), rows))).astype(np.float32)
+    sw = np.exp(rng.normal(size=(n, ref.blocks(N), ref.blocks(K)))).astype(np.float32)
+    want, size = ref.product(a, sa, counts, w, sw)
+    dropped = ref.product(a, sa, counts, w, sw, drop=True)[1]
+    for out in (torch.bfloat16, torch.float32):
+        y = torch.full((rows, N), -7.0, dtype=out, device="cuda")
+        mok.mok_block8_gemm(dev(a), dev(sa), rows, K, dev(w), dev(sw), N, y, offsets=offsets_of(counts), n_local=n)
+        tol = (K + 2) * 2.0 ** -23 * size + (2.0 ** -8 * np.abs(want) + dropped if out is torch.bfloat16 else
+                                            2.0 ** -24 * np.abs(want))
+        assert np.all(np.abs(host(y.float()) - want) <= tol)
 
 
 @pytest.mark.parametrize("counts,M,N", [([1500], 512, 1344), ([600, 700, 0, 800], 320, 768), ([300] * 20, 512, 576)])
