@@ -161,6 +161,34 @@ def test_muon_step(n, rows, cols, grads, nesterov, copy):
         assert torch.equal(pb, p.bfloat16())
 
 
+@pytest.mark.parametrize("n,rows,cols", [(12, 2040, 2176), (11, 2303, 2040)])
+def test_largest_tiles(n, rows, cols):
+    """Enough of the largest tiles for the chip in every product; the step and the update alone, against torch's fp64
+    products on the GPU, with the tolerances of test_muon_step and test_orthogonalise."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    normal = lambda: torch.randn(n, rows, cols, generator=gen, device="cuda")  # noqa: E731
+    g, p0, m0 = normal(), normal(), normal()
+    p, m, pb = p0.clone(), m0.clone(), torch.zeros(n, rows, cols, dtype=torch.bfloat16, device="cuda")
+    ws = workspace(n, rows, cols)
+    mok.mok_muon_step(p, g, m, n, rows, cols, ws, nesterov=0, p_bf16=pb, **HYPER)
+    out = torch.empty_like(pb)
+    mok.mok_orthogonalise(m, n, rows, cols, out, ws)
+    a, b, c = COEF
+    h = HYPER
+    assert torch.equal(pb, p.bfloat16())
+    for i in range(n):
+        v = m[i].double()
+        assert (v - (h["momentum"] * m0[i].double() + h["grad_scale"] * g[i].double())).abs().max() <= 4 * U * 8
+        y = v / v.norm()
+        for _ in range(5):
+            gram = y @ y.T.contiguous()
+            y = a * y + (b * gram + c * gram @ gram) @ y
+        assert (out[i].double() - y).norm() <= 2.0 ** -7 * y.norm()
+        want = p0[i].double() * (1 - h["lr"] * h["weight_decay"]) - h["lr"] * h["scale"] * y
+        size = 4 * U * p0[i].double().norm() + h["lr"] * h["scale"] * 2.0 ** -7 * y.norm()
+        assert (p[i].double() - want).norm() <= size
+
+
 def test_muon_scalars():
     """lr and grad_scale from the device, and a step that is skipped."""
     rng = np.random.default_rng(7)
