@@ -624,7 +624,12 @@ mok_status mok_dispatch_backward(const void* dx_slots, int32_t rows,
  *   weight operand  codes u8 [N][K], row-major; scales fp32
  *                   [ceil(N / 128)][ceil(K / 128)]: one for 128 x 128 values
  * K and N are multiples of 64, so a last block may be 64 wide.  Codes are
- * 16-byte aligned, scales 4-byte.
+ * 16-byte aligned, scales 4-byte.  n_local is 1..256.  What is larger than a
+ * launch can be is refused (MOK_ERR_UNSUPPORTED): more than 2^23 - 1 tiles of
+ * 128 x 128 values in a quantiser, mok_block8_slots(rows, n_local) / 128 *
+ * ceil(W / 128) of them for rows; more than 2^24 - 1 tiles in a product,
+ * (ceil(rows / 64) + n_local - 1) * ceil(N / 128), or in a gradient,
+ * n_local * ceil(M / 128) * ceil(N / 128).
  * Slot blocks: for products that contract over an expert's rows (the weight
  * gradients) operands lie transposed, codes [W][S] with S =
  * mok_block8_slots(rows, n_local): expert e's rows offsets[e] ..
@@ -690,7 +695,7 @@ mok_status mok_block8_quantise(const mok_block8_source* src, int32_t rows, int32
  * [n][N][K], with scales [n][ceil(N / 128)][ceil(K / 128)] by the rule above;
  * codes_t / scales_t (both or neither NULL): the same values as the transposed
  * matrices' operand, codes [n][K][N], scales [n][ceil(K / 128)][ceil(N / 128)]
- * (what the gradient of the product's input takes). */
+ * (what the gradient of the product's input takes).  n up to 65535. */
 mok_status mok_block8_quantise_weights(const void* w, int32_t type, int32_t n, int32_t N, int32_t K,
                                        uint8_t* codes, float* scales, uint8_t* codes_t,
                                        float* scales_t, hipStream_t stream);
@@ -714,7 +719,7 @@ mok_status mok_block8_gemm(const uint8_t* a, const float* a_scales, int32_t rows
  * dy_t: LINES [M][S], x_t: BLOCKS [N][S], both as mok_block8_quantise writes
  * them for `rows` and n_local; M and N multiples of 64; dw [n_local][M][N]
  * (out_type, summed as by mok_block8_gemm).  accumulate = 1 (fp32 dw): added to dw.  An expert without rows
- * gets zeros, or keeps its dw. */
+ * gets zeros, or keeps its dw.  S below 2^24. */
 mok_status mok_block8_wgrad(const uint8_t* dy_t, const float* dy_scales, int32_t M,
                             const uint8_t* x_t, const float* x_scales, int32_t N, int32_t rows,
                             const int32_t* offsets, int32_t n_local, void* dw, int32_t out_type,

@@ -209,9 +209,14 @@ size_t type_size(int32_t t) { return t == MOK_TYPE_BF16 ? 2 : 4; }
 constexpr int32_t kMaxRouteTokens = (1 << 26) - 4;
 constexpr int32_t kMaxBiasLayers = (1 << 22) - 1;
 
-// A launch has fewer than 2^32 threads; the block products' largest workgroup
-// has 512.  Their operands' rows stay below what 256 of them can be apart in 32 bits.
-constexpr int64_t kMaxWorkgroups = (1ll << 32) / 512 - 1;
+// A launch has fewer than 2^32 threads.  Quantisers have 512 for 128 x 128
+// values.  Products have the most workgroups in tiles of 64 x 128 and gradients in
+// tiles of 128 x 128, both of 256 threads; the large tiles have 512 and are
+// taken where they are fewer than half as many, the 32 x 32 ones up to two for a
+// CU of an even split of the rows.  Operands' rows stay below what 256 of them
+// can be apart in 32 bits.
+constexpr int64_t kMaxQuantisers = (1ll << 32) / 512 - 1, kMaxProducts = (1ll << 32) / 256 - 1;
+int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 constexpr int32_t kBlock8MaxK = 1 << 20, kBlock8MaxSlots = (1 << 24) - 1;
 
 bool block8_width(int32_t w) { return w > 0 && w % 64 == 0; }
@@ -329,8 +334,7 @@ mok_status mok_block8_quantise(const mok_block8_source* src, int32_t rows, int32
   if (odd(src->x, size) || odd(src->d, size) || odd(offsets, 4) || odd(codes, 16) || odd(scales, 4) ||
       odd(codes_t, 16) || odd(scales_t, 4))
     return MOK_ERR_INVALID_ARG;
-  const int64_t tiles = block8_slots(rows, n_local) / kBlock * ((W + kBlock - 1) / kBlock);
-  if (tiles > kMaxWorkgroups) return MOK_ERR_UNSUPPORTED;
+  if (block8_slots(rows, n_local) / kBlock * tiles_of(W, kBlock) > kMaxQuantisers) return MOK_ERR_UNSUPPORTED;
   return hip_status(launch_block8_quantise(*src, rows, W, offsets, n_local, codes, scales, codes_t,
                                            scales_t, t_scales == MOK_BLOCK8_BLOCKS, stream));
 }
@@ -342,8 +346,8 @@ mok_status mok_block8_quantise_weights(const void* w, int32_t type, int32_t n, i
   if ((n > 0 && (!w || !codes || !scales)) || !codes_t != !scales_t) return MOK_ERR_INVALID_ARG;
   if (odd(w, type_size(type)) || odd(codes, 16) || odd(scales, 4) || odd(codes_t, 16) || odd(scales_t, 4))
     return MOK_ERR_INVALID_ARG;
-  const int64_t tiles = static_cast<int64_t>((N + kBlock - 1) / kBlock) * ((K + kBlock - 1) / kBlock);
-  if (n > 65535 || tiles * n > kMaxWorkgroups) return MOK_ERR_UNSUPPORTED;
+  const int64_t tiles = tiles_of(N, kBlock) * tiles_of(K, kBlock);   // below 2^48
+  if (n > 65535 || (n > 0 && tiles > kMaxQuantisers / n)) return MOK_ERR_UNSUPPORTED;
   return hip_status(launch_block8_weights(w, type == MOK_TYPE_BF16, n, N, K, codes, scales, codes_t,
                                           scales_t, stream));
 }
@@ -358,7 +362,7 @@ mok_status mok_block8_gemm(const uint8_t* a, const float* a_scales, int32_t rows
   if (odd(a, 16) || odd(a_scales, 4) || odd(offsets, 4) || odd(w, 16) || odd(w_scales, 4) || odd(out, 16))
     return MOK_ERR_INVALID_ARG;
   if (K > kBlock8MaxK || static_cast<int64_t>(N) * K >= 1ll << 32 ||
-      block8_slots(rows, n_local) / 16 * ((N + 63) / 64) > kMaxWorkgroups)
+      (tiles_of(rows, 64) + n_local - 1) * tiles_of(N, 128) > kMaxProducts)
     return MOK_ERR_UNSUPPORTED;
   Block8Product p{};
   p.t = a; p.t_scales = a_scales; p.w = w; p.w_scales = w_scales;
@@ -378,7 +382,7 @@ mok_status mok_block8_wgrad(const uint8_t* dy_t, const float* dy_scales, int32_t
   if (odd(dy_t, 16) || odd(dy_scales, 4) || odd(x_t, 16) || odd(x_scales, 4) || odd(offsets, 4) || odd(dw, 16))
     return MOK_ERR_INVALID_ARG;
   const int64_t S = block8_slots(rows, n_local);
-  if (S > kBlock8MaxSlots || static_cast<int64_t>(n_local) * ((M + 63) / 64) * ((N + 63) / 64) > kMaxWorkgroups)
+  if (S > kBlock8MaxSlots || tiles_of(M, 128) * tiles_of(N, 128) > kMaxProducts / n_local)
     return MOK_ERR_UNSUPPORTED;
   Block8Product p{};
   p.t = dy_t; p.t_scales = dy_scales; p.w = x_t; p.w_scales = x_scales;
