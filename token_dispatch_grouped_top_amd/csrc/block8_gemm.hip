@@ -358,6 +358,7 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, const Job& j
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<float4*>(own + (lane & 31) * PITCH + 32 * i + 8 * g + 4 * (lane >> 5)) =
             make_float4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // lanes read others' values
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
       float4 v = *reinterpret_cast<const float4*>(own + (k * 64 + lane) / LPR * PITCH + (k * 64 + lane) % LPR * 4);
@@ -374,6 +375,7 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, const Job& j
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = v;
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");       // read before the next rows are written
   }
 }
 
@@ -452,7 +454,7 @@ __device__ __forceinline__ void block8_job(const Block8Product& p, int n_wt, uin
 
 template <class G, bool WGRAD, bool EXACT, bool SPLIT>
 __global__ __launch_bounds__(G::THREADS) void k_block8(const Block8Product p, int n_wt) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[G::LDS];
+  __shared__ __attribute__((aligned(kRow))) uint8_t lds[G::LDS];   // chunks of a row are told apart by address bits
   block8_job<G, WGRAD, EXACT, SPLIT>(p, n_wt, lds);
 }
 

@@ -653,6 +653,7 @@ __device__ __forceinline__ void muon_tile(const Product& p, uint8_t* __restrict_
           for (int i = 0; i < 2; ++i)
             *reinterpret_cast<float4*>(wide + fr * G::WIDE + 16 * k + 8 * fh + 4 * i) =
                 make_float4(f[k][4 * i], f[k][4 * i + 1], f[k][4 * i + 2], f[k][4 * i + 3]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // lanes read others' values
         const int64_t to0 = out0 + static_cast<int64_t>(32 * (b / G::FW)) * p.cols + 32 * (b % G::FW);
         uint16_t* half = EPI == LAST_OUT ? p.o : p.p_bf16;
         if (p.vec) {
@@ -689,6 +690,7 @@ __device__ __forceinline__ void muon_tile(const Product& p, uint8_t* __restrict_
             if (half) half[to] = f32_to_bf16(v);
           }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // read before the next block's are written
       }
     }
     if (b + AHEAD < BLOCKS) fetch(b + AHEAD);
