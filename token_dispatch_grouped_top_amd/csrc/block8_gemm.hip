@@ -175,7 +175,7 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, const Job& j
   auto issue_t = [&](int step, int b) {
     step = step < steps ? step : steps - 1;
     const bool cut = half && step == steps - 1;
-    static_assert(G::LT <= 4 && G::LW <= 8, "loads of a stage");
+    static_assert(G::LT <= 4 && G::LW <= 4 && G::LT != 3 && G::LW != 3, "loads of a stage");
     lt.template load<0>(stage_t(b), wave, step, cut);
     if constexpr (G::LT > 1) lt.template load<1>(stage_t(b), wave, step, cut);
     if constexpr (G::LT > 2) { lt.template load<2>(stage_t(b), wave, step, cut); lt.template load<3>(stage_t(b), wave, step, cut); }
@@ -189,10 +189,6 @@ __device__ __forceinline__ void block8_tile(const Block8Product& p, const Job& j
     lw.template load<0>(stage_w(b), wave, step, cut);
     if constexpr (G::LW > 1) lw.template load<1>(stage_w(b), wave, step, cut);
     if constexpr (G::LW > 2) { lw.template load<2>(stage_w(b), wave, step, cut); lw.template load<3>(stage_w(b), wave, step, cut); }
-    if constexpr (G::LW > 4) {
-      lw.template load<4>(stage_w(b), wave, step, cut); lw.template load<5>(stage_w(b), wave, step, cut);
-      lw.template load<6>(stage_w(b), wave, step, cut); lw.template load<7>(stage_w(b), wave, step, cut);
-    }
   };
 
   // ---- main loop
@@ -445,9 +441,9 @@ __device__ __forceinline__ void block8_job(const Block8Product& p, int n_wt, uin
     static_assert(G::TT == 256 && G::TW == 256 && G::WAVES == 8, "the parts of this tile");
     job.i0 += piece * (G::TW / pieces);
     if (job.i0 >= p.N) return;
-    if (pieces == 4) return block8_tile<Geo<256, 64, 8, 1, 2, true>, WGRAD, EXACT>(p, job, lds);
-    if (pieces == 2) return block8_tile<Geo<256, 128, 4, 2, 2, true>, WGRAD, EXACT>(p, job, lds);
-    if (job.t_all - job.t0 <= 128) return block8_tile<Geo<128, 256, 2, 4, 2, true>, WGRAD, EXACT>(p, job, lds);
+    if (pieces == 4) return block8_tile<Geo<256, 64, 8, 1, 2>, WGRAD, EXACT>(p, job, lds);
+    if (pieces == 2) return block8_tile<Geo<256, 128, 4, 2, 2>, WGRAD, EXACT>(p, job, lds);
+    if (job.t_all - job.t0 <= 128) return block8_tile<Geo<128, 256, 2, 4, 2>, WGRAD, EXACT>(p, job, lds);
   }
   block8_tile<G, WGRAD, EXACT>(p, job, lds);
 }
@@ -589,10 +585,10 @@ hipError_t run_thin(const Block8Product& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-using Big = Geo<256, 256, 2, 4, 2, true>;
-using Mid = Geo<64, 128, 1, 4, 3, true>;       // two to a CU
-using Mid16 = Geo<64, 128, 1, 4, 2, true>;     // fp16's products: three to a CU (85 us with two, 76 with three)
-using Out = Geo<128, 128, 2, 2, 2, true>;      // gradients: two to a CU, stores under other tiles' loads
+using Big = Geo<256, 256, 2, 4, 2>;
+using Mid = Geo<64, 128, 1, 4, 3>;       // two to a CU
+using Mid16 = Geo<64, 128, 1, 4, 2>;     // fp16's products: three to a CU (85 us with two, 76 with three)
+using Out = Geo<128, 128, 2, 2, 2>;      // gradients: two to a CU, stores under other tiles' loads
 
 // Tiles of an even split of the rows.
 template <class G> int64_t even_tiles(const Block8Product& p) {

@@ -1,8 +1,11 @@
-// nt_tile.h -- tile loop of products of two operands whose rows lie along the
-// contraction (both "row-major, K contiguous"): the 8-bit block products and
-// the fp16 products of the orthogonalised update.  A K-step is 128 bytes of a
-// row (128 E4M3 codes or 64 fp16 values): one cache line of HBM, 8 chunks of
-// 16 bytes in LDS.
+// nt_tile.h -- parts of products of two operands whose rows lie along the
+// contraction ("row-major, K contiguous"): what the 8-bit block products
+// (block8_gemm.hip) and the fp16 products of the orthogonalised update
+// (muon.hip) have in common -- types, the wait that ends a step, the order of a
+// step's reads, loads and matrix instructions -- and the tile shape and loader
+// of the former.  Each file has its own loop: the block products step by 128
+// bytes of a row (128 codes: one cache line of HBM, 8 chunks of 16 bytes in
+// LDS), the update by column blocks of 64 bytes (32 fp16 values).
 //
 // Roles: D[i][j] = sum_k W[i][k] T[j][k] with W the MFMA's first operand, so a
 // lane holds, for one row j of T, runs of four consecutive i.  An output whose
@@ -10,8 +13,9 @@
 //
 // Loads go straight to LDS (buffer loads with 16 bytes a lane, NS stages); a
 // row or chunk outside an operand reads as zero through the buffer's extent.
-// Chunk c of row r lies at place c ^ key(r), which a lane realises by what it
-// asks for, since the direct load puts lanes behind each other.
+// A chunk's place in its row depends on the row, which a lane realises by what
+// it asks for, since the direct load puts lanes behind each other; for 128-byte
+// rows chunk c of row r lies at place c ^ key(r).
 #pragma once
 
 #include "mok_internal.h"
@@ -24,7 +28,6 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
-typedef __attribute__((address_space(1))) const void* glb_ptr_t;
 
 constexpr int kRow = 128;                      // bytes of a row in a stage
 constexpr uint32_t kOutside = 0xfffffff0u;     // a buffer offset past every extent
@@ -56,20 +59,19 @@ template <int M, int A, int B, int m = 0> __device__ __forceinline__ void interl
   }
 }
 
-// TT x TW: rows of T and of W in a workgroup's tile; WT x WW waves; NS stages.
-// SCALES: 4-byte slots for scales in each stage.
-template <int TT_, int TW_, int WT_, int WW_, int NS_, bool SCALES_> struct Geo {
+// TT x TW: rows of T and of W in a workgroup's tile; WT x WW waves; NS stages,
+// each with a 4-byte slot for a scale a thread.
+template <int TT_, int TW_, int WT_, int WW_, int NS_> struct Geo {
   static constexpr int TT = TT_, TW = TW_, WT = WT_, WW = WW_, NS = NS_;
-  static constexpr bool SCALES = SCALES_;
   static constexpr int WAVES = WT * WW, THREADS = 64 * WAVES;
   static constexpr int FT = TT / WT / 32, FW = TW / WW / 32;       // 32-row fragments of a wave
   static constexpr int LT = TT * kRow / 1024 / WAVES, LW = TW * kRow / 1024 / WAVES;   // loads of a wave
-  static constexpr int LPS = LT + LW + (SCALES ? 1 : 0);
-  static constexpr int STAGE = (TT + TW) * kRow + (SCALES ? THREADS * 4 : 0);
+  static constexpr int LPS = LT + LW + 1;
+  static constexpr int STAGE = (TT + TW) * kRow + THREADS * 4;
   static constexpr int EPI = WAVES * 32 * (32 * FW + 4) * 4;       // a wave's 32 rows of fp32 results
   static constexpr int LDS = NS * STAGE > EPI ? NS * STAGE : EPI;
   static_assert(FT >= 1 && FW >= 1 && LT >= 1 && LW >= 1, "every wave loads and multiplies");
-  static_assert(!SCALES || TT + TW / 128 + 1 <= THREADS, "a thread for each scale");
+  static_assert(TT + TW / 128 + 1 <= THREADS, "a thread for each scale");
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
