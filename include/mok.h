@@ -623,8 +623,8 @@ mok_status mok_dispatch_backward(const void* dx_slots, int32_t rows,
  *                   j of row r at j * rows + r
  *   weight operand  codes u8 [N][K], row-major; scales fp32
  *                   [ceil(N / 128)][ceil(K / 128)]: one for 128 x 128 values
- * K and N are multiples of 64, so a last block may be 64 wide.  Codes are
- * 16-byte aligned, scales 4-byte.  n_local is 1..256.  What is larger than a
+ * K and N are multiples of 64, so a last block may be 64 wide.  Codes and the
+ * products' results are 16-byte aligned, scales 4-byte.  n_local is 1..256.  What is larger than a
  * launch can be is refused (MOK_ERR_UNSUPPORTED): more than 2^23 - 1 tiles of
  * 128 x 128 values in a quantiser, mok_block8_slots(rows, n_local) / 128 *
  * ceil(W / 128) of them for rows; more than 2^24 - 1 tiles in a product,
@@ -835,8 +835,8 @@ typedef struct {
     int32_t steps;       /* 1..32                                                */
 } mok_newton_schulz;
 
-/* Bytes of scratch of the two calls below; 0 for bad sizes.  rows and cols up
- * to 32768, n up to 65535.  Contents on entry do not matter. */
+/* Bytes of scratch (256-byte aligned) of the two calls below; 0 for bad sizes.
+ * rows and cols up to 32768, n up to 65535.  Contents on entry do not matter. */
 size_t mok_muon_workspace_size(int32_t n, int32_t rows, int32_t cols);
 
 /* out (bf16 [n][rows][cols]) = the orthogonalised x (mok_type, same shape).

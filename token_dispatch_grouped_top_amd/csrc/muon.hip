@@ -459,7 +459,11 @@ __device__ __forceinline__ void muon_tile(const Product& p, uint8_t* __restrict_
       // Sums go and come as relaxed atomics of the whole GPU, which pass by the
       // XCDs' own L2s: a release and an acquire would write back and drop all
       // that these hold (measured: 19 us for 384 x 7168 instead of 9).  The wait
-      // for the stores is what orders them before the count.
+      // for the stores is what orders them before the count, and the branch on the
+      // count what orders the loads behind it.  That is gfx950's way with such
+      // stores and loads (each complete when vmcnt has counted it, none served from
+      // an older line), an assumption on the hardware: the language promises it
+      // for release and acquire alone.
       constexpr int64_t EACH = static_cast<int64_t>(G::TT) * G::TW;
       float* mine = p.parts + (static_cast<int64_t>(t) * p.pieces + piece) * EACH + tid;
 #pragma unroll
@@ -720,8 +724,12 @@ template <class G, int EPI> hipError_t run(const Product& p, hipStream_t s) {
 // The largest tile that leaves no CU idle and little of itself past the edges.
 // Measured, all products of a call in one size: 2 x 4096 x 2048 256 x 128 tiles 883 us, 128 x 128 870,
 // 64 x 64 1069; 2048 x 7168 982, 811, 937; 1024 x 1024 324, 215, 143; 48 x 333 x
-// 190 (a third of each 128 x 128 tile past the edge) -, 139, 125; 384 x 7168, its last products in 168 tiles of
-// 128 x 128 160, in 64 x 64 151.
+// 190 (a third of each 128 x 128 tile past the edge) -, 139, 125.
+// Near the border, calls with B X in 128 x 128 tiles and in 64 x 64, all else alike: 128 tiles (1024 x 2048) 176, 167
+// us; 160 (512 x 5120) 155, 155; 168 (384 x 7168) 161, 157; 192 (512 x 6144) 158, 159, (768 x 4096) 170, 171, (12 x
+// 512 x 512) 144, 142; 200 (640 x 5120) 170, 182; 216 (24 x 384 x 384) 131, 136; 256 (1024 x 4096) 229, 237.  With
+// X X^T and G^2 in them: 108 tiles (3 x 1024 x 1024) 221, 195; 120 (12 x 512 x 512) 163, 142; 144 (4 x 1024 x 1024) 248,
+// 246; 156 (2 x 1536 x 1536) 334, 340; 160 (16 x 512 x 512) 180, 175.
 template <int EPI> hipError_t run(Product p, hipStream_t s) {
   p.pieces = 1;
   const int64_t half = tiles_of<Half, EPI>(p), mid = tiles_of<Mid, EPI>(p), small = tiles_of<Small, EPI>(p);
