@@ -648,7 +648,7 @@ mok_status mok_dispatch_backward(const void* dx_slots, int32_t rows,
  *                          x[r][c], u = x[r][I + c] (x: h) and da = d[r][c] (d: I
  *                          wide), dg = da u s (1 + g (1 - s)) in column c, du =
  *                          da g s in column I + c, s = 1 / (1 + e^-g)
- * (fp32 arithmetic). */
+ * (fp32 arithmetic; e^-|g| with |g| 2^-24 of it besides). */
 typedef enum {
     MOK_BLOCK8_COPY = 0, MOK_BLOCK8_SWIGLU = 1, MOK_BLOCK8_SWIGLU_BWD = 2
 } mok_block8_op;
